@@ -19,8 +19,17 @@ The group-wise 4-bit form with a 16-bit low-rank branch (include/hq_gw.h):
     hq_gw_quantize_act(desc, X, sigma_inv, l1s, a_codes, a_scale, u, workspace)
     hq_gw_linear(desc, a_codes, a_scale, u, w_codes, w_scale, l2b, bias_f32, Y)
 
+The operators beside the layer (include/hq_ops.h): products with an
+activation, a gate and a residual in their epilogue, and the group norm:
+
+    hq_linear_ep(desc, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32, epilogue, Y, acc_debug)
+    hq_dense(desc, X, W, bias, epilogue, Y)
+    hq_group_norm(desc, X, gamma, beta, Y, workspace)
+
 `HadamardQuantLinear` and `GroupWiseQuantLinear` bundle the caller-side
-buffers of one layer of each form.
+buffers of one layer of each form; `DenseLinear` and `GroupNorm` the weights of
+a 16-bit layer and of a group norm; `PointwiseBlock` a group norm and the
+quantized 1x1 convolution it feeds.
 """
 from __future__ import annotations
 
@@ -42,6 +51,9 @@ __all__ = [
     "HadamardQuantLinear", "GwDesc", "hq_gw_scale_ld", "hq_gw_sigma_inv", "hq_gw_prepare_weights",
     "hq_gw_quantize_act", "hq_gw_linear", "hq_gw_debug_linear_f32", "GroupWiseQuantLinear",
     "hq_debug_last_cuda_error", "hq_gw_quantize_act_workspace_bytes",
+    "HQ_ACT_NONE", "HQ_ACT_RELU", "HQ_ACT_SILU", "HQ_ACT_GELU", "HQ_ACT_GELU_TANH", "Epilogue",
+    "DenseDesc", "GroupNormDesc", "hq_linear_ep", "hq_dense", "hq_group_norm",
+    "hq_group_norm_workspace_bytes", "DenseLinear", "GroupNorm", "PointwiseBlock",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +64,7 @@ HQ_CENTER_NONE, HQ_CENTER_TOKEN_MEAN, HQ_CENTER_TOKEN_MEAN_PRE = 0, 1, 2
 HQ_CODES_I8, HQ_CODES_I4_PACKED = 0, 1
 HQ_FAULT_NONE, HQ_FAULT_QUANT_WITHHOLD_ROW = 0, 1
 HQ_GEMM_AUTO, HQ_GEMM_SINGLE_CTA, HQ_GEMM_CTA_PAIR = 0, 1, 2
+HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "HQ_OK", 1: "HQ_ERR_INVALID_ARGUMENT", 2: "HQ_ERR_UNSUPPORTED",
                 3: "HQ_ERR_MISALIGNED", 4: "HQ_ERR_CUDA", 5: "HQ_ERR_TIMEOUT",
                 6: "HQ_ERR_DEVICE"}
@@ -62,7 +75,8 @@ EXPORTED = ("hq_status_string", "hq_version", "hq_calib_act_absmax", "hq_prepare
             "hq_debug_mma_ceiling", "hq_debug_tmap_cache", "hq_gw_scale_ld", "hq_gw_sigma_inv",
             "hq_gw_prepare_weights", "hq_gw_quantize_act", "hq_gw_linear",
             "hq_gw_debug_linear_f32", "hq_debug_last_cuda_error",
-            "hq_gw_quantize_act_workspace_bytes")
+            "hq_gw_quantize_act_workspace_bytes", "hq_linear_ep", "hq_dense", "hq_group_norm",
+            "hq_group_norm_workspace_bytes")
 
 
 class HQError(RuntimeError):
@@ -93,6 +107,39 @@ class GwDesc(ctypes.Structure):
 
     def __init__(self, K, N, group=64, rank=32, a_bits=4, w_bits=4):
         super().__init__(K, N, group, rank, a_bits, w_bits)
+
+
+class DenseDesc(ctypes.Structure):
+    """hq_dense_desc (host memory): a 16-bit linear layer."""
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32)]
+
+    def __init__(self, K, N):
+        super().__init__(K, N)
+
+
+class GroupNormDesc(ctypes.Structure):
+    """hq_group_norm_desc (host memory)."""
+    _fields_ = [("C", ctypes.c_int32), ("groups", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+    def __init__(self, C, groups, act=HQ_ACT_NONE, eps=1e-5):
+        super().__init__(C, groups, act, eps)
+
+
+class Epilogue(ctypes.Structure):
+    """hq_epilogue (host memory): Y = residual + gate[t // gate_rows] * act(z).
+
+    residual bf16 [T, N] and gate bf16 [ceil(T / gate_rows), N] are CUDA
+    tensors or None; the object keeps them alive."""
+    _fields_ = [("act", ctypes.c_int32), ("_residual", ctypes.c_void_p),
+                ("_gate", ctypes.c_void_p), ("gate_rows", ctypes.c_int64)]
+
+    def __init__(self, act=HQ_ACT_NONE, residual=None, gate=None, gate_rows=0):
+        if gate is not None and gate_rows < 1:
+            raise ValueError("a gate needs gate_rows >= 1 (rows of Y per row of the gate)")
+        super().__init__(act, None if residual is None else _ptr(residual),
+                         None if gate is None else _ptr(gate), gate_rows)
+        self.residual, self.gate = residual, gate
 
 
 _lib = None
@@ -160,6 +207,18 @@ def load_library():
         lib.hq_gw_debug_linear_f32.argtypes = list(lib.hq_gw_linear.argtypes)
         for name in ("hq_gw_sigma_inv", "hq_gw_prepare_weights", "hq_gw_quantize_act",
                      "hq_gw_linear", "hq_gw_debug_linear_f32"):
+            getattr(lib, name).restype = ctypes.c_int
+        ep_p = ctypes.POINTER(Epilogue)
+        lib.hq_linear_ep.argtypes = [desc_p, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     ep_p, _vp, _vp, _vp]
+        lib.hq_dense.argtypes = [ctypes.POINTER(DenseDesc), _vp, ctypes.c_int64, _vp, _vp, ep_p,
+                                 _vp, _vp]
+        gn_p = ctypes.POINTER(GroupNormDesc)
+        lib.hq_group_norm_workspace_bytes.argtypes = [gn_p, ctypes.c_int64, ctypes.c_int64]
+        lib.hq_group_norm_workspace_bytes.restype = ctypes.c_size_t
+        lib.hq_group_norm.argtypes = [gn_p, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp,
+                                      _vp, ctypes.c_size_t, _vp]
+        for name in ("hq_linear_ep", "hq_dense", "hq_group_norm"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("hq_calib_act_absmax", "hq_prepare_weights", "hq_quantize_act", "hq_linear",
                      "hq_forward_host",
@@ -403,6 +462,131 @@ def hq_gw_debug_linear_f32(desc: GwDesc, a_codes, a_scale, u, w_codes, w_scale, 
 
 
 # ---------------------------------------------------------------------------
+# the operators beside the layer (include/hq_ops.h), same names
+# ---------------------------------------------------------------------------
+# These check dtypes, shapes and devices, and run on the tensors' device (its
+# current stream when none is given), whichever device is current.
+
+def _tensor(t, name, dtype, shape, dev):
+    """The address of a contiguous CUDA tensor of this dtype, shape and device
+    index (None stays None)."""
+    if t is None:
+        return None
+    if (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must live in CUDA device memory")
+    return dev
+
+
+def _launch(dev, stream, call, where):
+    """call(stream handle) with device `dev` current."""
+    import torch
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, call, where)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    status = call(stream)
+    if status:
+        _check(status, where)
+
+
+def _epilogue_ref(ep, T, N, dev):
+    """By-reference argument of an Epilogue (or None) for a [T, N] output."""
+    import torch
+    if ep is None:
+        return None
+    if ep.residual is not None:
+        _tensor(ep.residual, "residual", torch.bfloat16, (T, N), dev)
+    if ep.gate is not None:
+        _tensor(ep.gate, "gate", torch.bfloat16, (-(-T // ep.gate_rows), N), dev)
+    return ctypes.byref(ep)
+
+
+def hq_linear_ep(desc: LayerDesc, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
+                 epilogue, Y, acc_debug=None, stream=None):
+    """hq_linear with an Epilogue (None: hq_linear itself)."""
+    import torch
+    f32, T, K, N = torch.float32, a_codes.shape[0], desc.K, desc.N
+    dev = _device_of(a_codes, "a_codes")
+    if desc.code_format == HQ_CODES_I4_PACKED:
+        a = _tensor(a_codes, "a_codes", torch.uint8, (T, K // 2), dev)
+    else:
+        a = _tensor(a_codes, "a_codes", torch.int8, (T, K), dev)
+    sx = _tensor(a_scale, "a_scale", f32, (T if desc.act_gran == HQ_PER_TOKEN else 1,), dev)
+    m = _tensor(a_mean, "a_mean", f32, (T,), dev)
+    w = _tensor(w_codes, "w_codes", torch.int8, (N, K), dev)
+    sw = _tensor(w_scale, "w_scale", f32, (N,), dev)
+    cs = _tensor(colsum, "colsum", f32, (N,), dev)
+    b = _tensor(bias_f32, "bias_f32", f32, (N,), dev)
+    y = _tensor(Y, "Y", torch.bfloat16, (T, N), dev)
+    acc = _tensor(acc_debug, "acc_debug", torch.int32, (T, N), dev)
+    ep = _epilogue_ref(epilogue, T, N, dev)
+    fn = load_library().hq_linear_ep
+    _launch(dev, stream, lambda st: fn(ctypes.byref(desc), T, a, sx, m, w, sw, cs, b, ep, y, acc,
+                                       st), "hq_linear_ep")
+
+
+def hq_dense(desc: DenseDesc, X, W, bias, epilogue, Y, stream=None):
+    """Y = residual + gate * act(X W^T + bias) in bf16 (epilogue None: the
+    product plus bias)."""
+    import torch
+    bf16, T = torch.bfloat16, X.shape[0]
+    dev = _device_of(X, "X")
+    x = _tensor(X, "X", bf16, (T, desc.K), dev)
+    w = _tensor(W, "W", bf16, (desc.N, desc.K), dev)
+    b = _tensor(bias, "bias", bf16, (desc.N,), dev)
+    y = _tensor(Y, "Y", bf16, (T, desc.N), dev)
+    ep = _epilogue_ref(epilogue, T, desc.N, dev)
+    fn = load_library().hq_dense
+    _launch(dev, stream, lambda st: fn(ctypes.byref(desc), x, T, w, b, ep, y, st), "hq_dense")
+
+
+def hq_group_norm_workspace_bytes(desc: GroupNormDesc, B: int, S: int) -> int:
+    return int(load_library().hq_group_norm_workspace_bytes(ctypes.byref(desc), int(B), int(S)))
+
+
+def hq_group_norm(desc: GroupNormDesc, X, gamma, beta, Y, workspace=None, stream=None):
+    """Y = act(group norm of X) over channels-last X [B, ..., C]; workspace: a
+    uint8 tensor of hq_group_norm_workspace_bytes(desc, B, S) bytes (S: the
+    product of the dimensions between) where that is not 0."""
+    import torch
+    bf16, C = torch.bfloat16, desc.C
+    if X.dim() < 2 or X.shape[-1] != C:
+        raise ValueError(f"X must have shape [B, ..., {C}], got {tuple(X.shape)}")
+    dev = _device_of(X, "X")
+    B = X.shape[0]
+    S = 1
+    for n in X.shape[1:-1]:
+        S *= n
+    x = _tensor(X, "X", bf16, X.shape, dev)
+    g = _tensor(gamma, "gamma", bf16, (C,), dev)
+    b = _tensor(beta, "beta", bf16, (C,), dev)
+    y = _tensor(Y, "Y", bf16, X.shape, dev)
+    ws, nws = None, 0
+    if workspace is not None:
+        nws = workspace.numel()
+        ws = _tensor(workspace, "workspace", torch.uint8, (nws,), dev)
+    fn = load_library().hq_group_norm
+    _launch(dev, stream, lambda st: fn(ctypes.byref(desc), x, B, S, g, b, y, ws, nws, st),
+            "hq_group_norm")
+
+
+# ---------------------------------------------------------------------------
 # one layer's caller-side buffers
 # ---------------------------------------------------------------------------
 
@@ -472,13 +656,18 @@ class HadamardQuantLinear:
                         b["a_scale"], b["a_mean"], self.workspace)
         return b
 
-    def forward(self, X, Y=None, acc_debug=None):
+    def forward(self, X, Y=None, acc_debug=None, epilogue=None):
+        """epilogue: an Epilogue for the product's output (hq_linear_ep)."""
         import torch
         T = X.shape[0]
         if Y is None:
             Y = torch.empty((T, self.desc.N), dtype=torch.bfloat16, device=X.device)
         b = self.quantize(X)
         mean = b["a_mean"] if self.desc.centering != HQ_CENTER_NONE else None
+        if epilogue is not None:
+            hq_linear_ep(self.desc, b["a_codes"], b["a_scale"], mean, self.w_codes, self.w_scale,
+                         self.colsum, self.bias_f32, epilogue, Y, acc_debug)
+            return Y
         hq_linear(self.desc, b["a_codes"], b["a_scale"], mean, self.w_codes, self.w_scale,
                   self.colsum, self.bias_f32, Y, acc_debug)
         return Y
@@ -686,3 +875,85 @@ class GroupWiseQuantLinear:
 
     __call__ = forward
 
+
+class DenseLinear:
+    """A linear layer in 16 bits (hq_dense): weight bf16 [N, K], bias bf16 [N]
+    or None, and an activation (HQ_ACT_*)."""
+
+    def __init__(self, weight, bias=None, act=HQ_ACT_NONE):
+        self.weight, self.bias, self.act = weight, bias, act
+        self.desc = DenseDesc(weight.shape[1], weight.shape[0])
+
+    def forward(self, X, Y=None, residual=None, gate=None, gate_rows=0):
+        """X bf16 [T, K] -> Y [T, N] = residual + gate[t // gate_rows] * act(X W^T + b)."""
+        import torch
+        if Y is None:
+            Y = torch.empty((X.shape[0], self.desc.N), dtype=torch.bfloat16, device=X.device)
+        ep = None
+        if self.act != HQ_ACT_NONE or residual is not None or gate is not None:
+            ep = Epilogue(self.act, residual, gate, gate_rows)
+        hq_dense(self.desc, X, self.weight, self.bias, ep, Y)
+        return Y
+
+    __call__ = forward
+
+
+class GroupNorm:
+    """A group norm with an activation over channels-last activations
+    (hq_group_norm): gamma and beta bf16 [C] or None."""
+
+    def __init__(self, channels, groups, gamma=None, beta=None, eps=1e-5, act=HQ_ACT_NONE):
+        self.desc = GroupNormDesc(channels, groups, act, eps)
+        self.gamma, self.beta = gamma, beta
+
+    def forward(self, X, Y=None):
+        """X bf16 [B, ..., C] -> Y of the same shape (Y may be X).  The
+        workspace comes from PyTorch's allocator at every call, on the current
+        stream, so calls on several streams share none."""
+        import torch
+        if Y is None:
+            Y = torch.empty_like(X)
+        B, C = X.shape[0], self.desc.C
+        n = X.numel()
+        ws = None
+        if n:
+            nb = hq_group_norm_workspace_bytes(self.desc, B, n // (B * C))
+            if nb:
+                ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
+        hq_group_norm(self.desc, X, self.gamma, self.beta, Y, ws)
+        return Y
+
+    __call__ = forward
+
+
+class PointwiseBlock:
+    """A normalized, quantized 1x1 convolution over channels-last pixels:
+
+        Y = [X +] linear(act(group_norm(X)))
+
+    `norm` is a GroupNorm and `linear` a HadamardQuantLinear (or a
+    GroupWiseQuantLinear without residual or act) whose K is the norm's channel
+    count; residual=True adds the block's input, in the product's epilogue (N
+    must equal K); act is the product's own activation."""
+
+    def __init__(self, norm: GroupNorm, linear, residual=False, act=HQ_ACT_NONE):
+        K, N = linear.desc.K, linear.desc.N
+        if norm.desc.C != K:
+            raise ValueError(f"the norm has {norm.desc.C} channels, the layer takes {K}")
+        if residual and N != K:
+            raise ValueError(f"a residual needs as many outputs as inputs, got {K} -> {N}")
+        if (residual or act != HQ_ACT_NONE) and not isinstance(linear, HadamardQuantLinear):
+            raise ValueError("an epilogue needs a HadamardQuantLinear")
+        self.norm, self.linear, self.residual, self.act = norm, linear, residual, act
+
+    def forward(self, X):
+        """X bf16 [B, ..., K] -> [B, ..., N]."""
+        h = self.norm(X).view(-1, self.norm.desc.C)
+        if self.residual or self.act != HQ_ACT_NONE:
+            ep = Epilogue(self.act, X.view(-1, X.shape[-1]) if self.residual else None)
+            Y = self.linear.forward(h, epilogue=ep)
+        else:
+            Y = self.linear.forward(h)
+        return Y.view(*X.shape[:-1], self.linear.desc.N)
+
+    __call__ = forward

@@ -1,0 +1,103 @@
+// hq_act.cuh -- the activations of the fused epilogues and of the group norm,
+// in fp32 on pairs of values, and bf16 pair packing.
+//
+// silu and both gelus are z * sigmoid(u(z)) with sigmoid(u) = 1 / (1 + 2^(-u log2 e)):
+// one exponential and one reciprocal instruction a value.
+//   silu       u = z
+//   gelu_tanh  0.5 (1 + tanh v) = sigmoid(2 v), so u = 2 sqrt(2/pi) (z + 0.044715 z^3)
+//   gelu       u = log(Phi(z) / Phi(-z)), an odd function of z: z P(z^2) with P
+//              of degree 8, a least-squares fit reweighted towards the largest
+//              deviation of u over |z| <= 5.5.  |u| is then off by at most
+//              1.4e-5 in fp32, so Phi is within 1.4e-5 of its value relative
+//              to itself, on both sides.  Beyond 5.5 P stays at its end
+//              value: u grows linearly and z Phi(z) < 1.1e-7 in magnitude on
+//              the negative side, as is what the formula gives there.
+// relu keeps a NaN (the comparison is false).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "hq_device.cuh"
+
+namespace hq {
+
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ f2 unpack_bf16x2(uint32_t v) {
+  return pk(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// z * sigmoid(u), with u already times -log2 e
+__device__ __forceinline__ f2 mul_sigmoid(f2 z, f2 minus_u_log2e) {
+  const f2 d = add2(pk(1.0f, 1.0f), pk(ex2_approx(minus_u_log2e.x), ex2_approx(minus_u_log2e.y)));
+  return mul2(z, pk(rcp_approx(d.x), rcp_approx(d.y)));
+}
+
+__device__ __forceinline__ f2 act_silu(f2 z) {
+  return mul_sigmoid(z, mul2(z, pk(-1.4426950408889634f, -1.4426950408889634f)));
+}
+
+__device__ __forceinline__ f2 act_gelu_tanh(f2 z) {
+  // -2 sqrt(2/pi) log2 e (z + 0.044715 z^3)
+  constexpr float a = -2.3022082f, b = -0.10294324f;
+  const f2 t = mul2(z, z);
+  return mul_sigmoid(z, mul2(z, fma2(t, pk(b, b), pk(a, a))));
+}
+
+__device__ __forceinline__ f2 act_gelu(f2 z) {
+  const f2 t0 = mul2(z, z);
+  const f2 t = pk(fminf(t0.x, 30.25f), fminf(t0.y, 30.25f));
+  f2 q = pk(9.91229884630962e-13f, 9.91229884630962e-13f);
+  q = fma2(q, t, pk(-1.5642973028029417e-10f, -1.5642973028029417e-10f));
+  q = fma2(q, t, pk(1.0629670477158015e-08f, 1.0629670477158015e-08f));
+  q = fma2(q, t, pk(-4.0455273619954824e-07f, -4.0455273619954824e-07f));
+  q = fma2(q, t, pk(9.244396096619312e-06f, 9.244396096619312e-06f));
+  q = fma2(q, t, pk(-0.00011615729454206303f, -0.00011615729454206303f));
+  q = fma2(q, t, pk(-5.883523772354238e-05f, -5.883523772354238e-05f));
+  q = fma2(q, t, pk(0.07267936319112778f, 0.07267936319112778f));
+  q = fma2(q, t, pk(1.5957502126693726f, 1.5957502126693726f));
+  const f2 u = mul2(z, q);
+  return mul_sigmoid(z, mul2(u, pk(-1.4426950408889634f, -1.4426950408889634f)));
+}
+
+__device__ __forceinline__ f2 act_relu(f2 z) {
+  return pk(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
+}
+
+// n pairs in place; `act` is uniform over the launch
+template <int N>
+__device__ __forceinline__ void act_chunk(int act, f2 (&z)[N]) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = act_silu(z[i]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = act_gelu(z[i]);
+  } else if (act == kActGeluTanh) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = act_gelu_tanh(z[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = act_relu(z[i]);
+  }
+}
+
+}  // namespace hq

@@ -10,6 +10,7 @@
 
 #include "../../include/hq.h"
 #include "../../include/hq_gw.h"
+#include "../../include/hq_ops.h"
 #include "hq_kernels.h"
 
 namespace hq {
@@ -732,6 +733,141 @@ hq_status check_linear_args(const hq_layer_desc* desc, int64_t T, const int8_t* 
 
 
 // ---------------------------------------------------------------------------
+// Epilogues and the operators beside the layer (include/hq_ops.h).
+bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
+
+constexpr int64_t kMaxEpRows = (int64_t(1) << 31) - 256;  // row coordinates are int32
+
+bool known_act(int act) { return act >= HQ_ACT_NONE && act <= HQ_ACT_GELU_TANH; }
+
+// The epilogue's own rules; Y bf16 [T,N].  T == 0: pointers are not looked at.
+hq_status check_epilogue(const hq_epilogue* ep, int64_t T, int N, const uint16_t* Y) {
+  if (ep == nullptr) return HQ_OK;
+  if (!known_act(ep->act)) return HQ_ERR_INVALID_ARGUMENT;
+  if (ep->gate != nullptr && ep->gate_rows < 1) return HQ_ERR_INVALID_ARGUMENT;
+  if (T == 0) return HQ_OK;
+  if ((ep->residual && !aligned16(ep->residual)) || (ep->gate && !aligned16(ep->gate)))
+    return HQ_ERR_MISALIGNED;
+  const uint64_t bytes = uint64_t(T) * uint64_t(N) * 2u;
+  if (ep->residual != Y && overlaps(Y, bytes, ep->residual, bytes)) return HQ_ERR_INVALID_ARGUMENT;
+  if (ep->gate != nullptr) {
+    const uint64_t rows = uint64_t((T - 1) / ep->gate_rows + 1);
+    if (overlaps(Y, bytes, ep->gate, rows * uint64_t(N) * 2u)) return HQ_ERR_INVALID_ARGUMENT;
+  }
+  return HQ_OK;
+}
+
+bool plain_epilogue(const hq_epilogue* ep) {
+  return ep == nullptr ||
+         (ep->act == HQ_ACT_NONE && ep->residual == nullptr && ep->gate == nullptr);
+}
+
+// Co-resident clusters of the CTA-pair GEMMs on the current device (0: none).
+int pair_clusters(DeviceState* dev) {
+  if (dev->pair_clusters < 0) {
+    int c = 0;
+    if (gemm_pair_max_clusters(&c) != cudaSuccess) {
+      (void)cudaGetLastError();
+      c = 0;
+    }
+    dev->pair_clusters = c;
+  }
+  return dev->pair_clusters;
+}
+
+// The integer GEMM behind hq_linear and hq_linear_ep (arguments checked, T > 0);
+// `ep` is null for the plain epilogue.
+hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
+                      const float* a_scale, const float* a_mean, const int8_t* w_codes,
+                      const float* w_scale, const float* colsum, const float* bias_f32,
+                      const hq_epilogue* ep, uint16_t* Y, int32_t* acc_debug, hq_stream_t stream) {
+  hq_status s;
+  DeviceState* dev;
+  s = device_state(&dev);
+  if (s != HQ_OK) return s;
+  const int K = desc->K, N = desc->N;
+  const int clusters_max = pair_clusters(dev);
+  int variant;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    variant = g_gemm_variant;
+  }
+  // weight-only Hadamard form: output blocks of m = out_order columns
+  const int m = desc->out_order > 1 ? desc->out_order : 1;
+  const int logo = ilog2_exact(m);
+  const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
+  if (variant == HQ_GEMM_CTA_PAIR && clusters_max <= 0 && logo == 0) return HQ_ERR_UNSUPPORTED;
+  const GemmChoice gc =
+      choose_gemm(T, N, K, dev->sm_count, clusters_max, variant, logo, packed);
+  const int bn = gc.pair ? 256 : gc.bn;
+  CUtensorMap ta, tb, ty;
+  s = packed ? encode_packed_a(&ta, a_codes, T, K) : encode_kmajor_i8(&ta, a_codes, T, K, 128);
+  if (s != HQ_OK) return s;
+  s = encode_kmajor_i8(&tb, w_codes, N, K, gc.pair ? 128 : bn);
+  if (s != HQ_OK) return s;
+  s = encode_out_bf16(&ty, Y, T, N);
+  if (s != HQ_OK) return s;
+  GemmEpParams p;  // the plain kernels take its GemmParams part
+  std::memset(&p, 0, sizeof(p));
+  CUtensorMap tr;
+  const void* tmap_r = nullptr;
+  if (ep != nullptr) {
+    p.act = ep->act;
+    p.gate = ep->gate;
+    p.gate_rows = ep->gate_rows;
+    if (ep->residual != nullptr) {
+      if ((s = encode_out_bf16(&tr, ep->residual, T, N)) != HQ_OK) return s;
+      tmap_r = &tr;
+    }
+  }
+  p.a_scale = a_scale;
+  p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
+  {
+    // |acc| <= 2^(a_bits-1) * 2^(w_bits-1) * K for codes within their declared
+    // widths, 16 times that for packed codes (widened to 16 * code)
+    const double bound = std::ldexp(1.0, desc->a_bits - 1) * std::ldexp(1.0, desc->w_bits - 1) *
+                         K * (packed ? 16.0 : 1.0);
+    p.small_acc = bound < 4194304.0 ? 1 : 0;
+  }
+  p.acc_unit = packed ? 0.0625f : 1.0f;
+  p.acc_shift = packed ? 4 : 0;
+  p.a_mean = a_mean;
+  p.w_scale = w_scale;
+  p.colsum = colsum;
+  p.bias = bias_f32;
+  p.Y = Y;
+  p.acc_debug = acc_debug;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.inv_sqrt_out = float(1.0 / std::sqrt(double(m)));
+  p.err = dev->err;
+  p.wait_ns = wait_ns();
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // tile order: groups of kGroupM M tiles (shared A and B tiles stay in L2)
+  p.group_m = kGroupM;
+  if (gc.pair) {
+    p.num_m_tiles = int((T + 255) / 256);
+    p.num_n_tiles = (N + 255) / 256;
+    const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
+    const int clusters = int(tiles < clusters_max ? tiles : clusters_max);
+    if (ep != nullptr)
+      return from_cuda(launch_gemm_pair_ep(false, &ta, &tb, &ty, tmap_r, p, clusters, st));
+    return from_cuda(launch_gemm_pair(&ta, &tb, &ty, p, clusters, st));
+  }
+  p.num_m_tiles = int((T + 127) / 128);
+  p.num_n_tiles = (N + bn - 1) / bn;
+  const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
+  const int grid = int(tiles < dev->sm_count ? tiles : dev->sm_count);
+  if (ep != nullptr)
+    return from_cuda(launch_gemm_ep(false, bn, logo, packed, &ta, &tb, &ty, tmap_r, p, grid, st));
+  return from_cuda(launch_gemm(bn, logo, packed, &ta, &tb, &ty, p, grid, st));
+}
+
+// ---------------------------------------------------------------------------
 // Group-wise form: tensor maps and shape rules.
 hq_status check_gw_desc(const hq_gw_desc* d) {
   if (d == nullptr) return HQ_ERR_INVALID_ARGUMENT;
@@ -1036,81 +1172,11 @@ hq_status hq_linear(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
                     const float* a_scale, const float* a_mean, const int8_t* w_codes,
                     const float* w_scale, const float* colsum, const float* bias_f32, uint16_t* Y,
                     int32_t* acc_debug, hq_stream_t stream) {
-  hq_status s = check_linear_args(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum,
-                                  bias_f32, Y, acc_debug);
+  const hq_status s = check_linear_args(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum,
+                                        bias_f32, Y, acc_debug);
   if (s != HQ_OK || T == 0) return s;
-  DeviceState* dev;
-  s = device_state(&dev);
-  if (s != HQ_OK) return s;
-  const int K = desc->K, N = desc->N;
-  if (dev->pair_clusters < 0) {
-    int c = 0;
-    if (gemm_pair_max_clusters(&c) != cudaSuccess) {
-      (void)cudaGetLastError();
-      c = 0;
-    }
-    dev->pair_clusters = c;
-  }
-  int variant;
-  {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    variant = g_gemm_variant;
-  }
-  // weight-only Hadamard form: output blocks of m = out_order columns
-  const int m = desc->out_order > 1 ? desc->out_order : 1;
-  const int logo = ilog2_exact(m);
-  const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
-  if (variant == HQ_GEMM_CTA_PAIR && dev->pair_clusters <= 0 && logo == 0) return HQ_ERR_UNSUPPORTED;
-  const GemmChoice gc =
-      choose_gemm(T, N, K, dev->sm_count, dev->pair_clusters, variant, logo, packed);
-  const int bn = gc.pair ? 256 : gc.bn;
-  CUtensorMap ta, tb, ty;
-  s = packed ? encode_packed_a(&ta, a_codes, T, K) : encode_kmajor_i8(&ta, a_codes, T, K, 128);
-  if (s != HQ_OK) return s;
-  s = encode_kmajor_i8(&tb, w_codes, N, K, gc.pair ? 128 : bn);
-  if (s != HQ_OK) return s;
-  s = encode_out_bf16(&ty, Y, T, N);
-  if (s != HQ_OK) return s;
-  GemmParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.a_scale = a_scale;
-  p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
-  {
-    // |acc| <= 2^(a_bits-1) * 2^(w_bits-1) * K for codes within their declared
-    // widths, 16 times that for packed codes (widened to 16 * code)
-    const double bound = std::ldexp(1.0, desc->a_bits - 1) * std::ldexp(1.0, desc->w_bits - 1) *
-                         K * (packed ? 16.0 : 1.0);
-    p.small_acc = bound < 4194304.0 ? 1 : 0;
-  }
-  p.acc_unit = packed ? 0.0625f : 1.0f;
-  p.acc_shift = packed ? 4 : 0;
-  p.a_mean = a_mean;
-  p.w_scale = w_scale;
-  p.colsum = colsum;
-  p.bias = bias_f32;
-  p.Y = Y;
-  p.acc_debug = acc_debug;
-  p.T = T;
-  p.N = N;
-  p.K = K;
-  p.inv_sqrt_out = float(1.0 / std::sqrt(double(m)));
-  p.err = dev->err;
-  p.wait_ns = wait_ns();
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // tile order: groups of kGroupM M tiles (shared A and B tiles stay in L2)
-  p.group_m = kGroupM;
-  if (gc.pair) {
-    p.num_m_tiles = int((T + 255) / 256);
-    p.num_n_tiles = (N + 255) / 256;
-    const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
-    const int clusters = int(tiles < dev->pair_clusters ? tiles : dev->pair_clusters);
-    return from_cuda(launch_gemm_pair(&ta, &tb, &ty, p, clusters, st));
-  }
-  p.num_m_tiles = int((T + 127) / 128);
-  p.num_n_tiles = (N + bn - 1) / bn;
-  const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
-  const int grid = int(tiles < dev->sm_count ? tiles : dev->sm_count);
-  return from_cuda(launch_gemm(bn, logo, packed, &ta, &tb, &ty, p, grid, st));
+  return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
+                     nullptr, Y, acc_debug, stream);
 }
 
 hq_status hq_forward_host(const hq_layer_desc* desc, const uint16_t* X_host, int64_t T,
@@ -1528,6 +1594,160 @@ hq_status hq_gw_debug_linear_f32(const hq_gw_desc* desc, int64_t T, const uint8_
   if (Y32 == nullptr) return HQ_ERR_INVALID_ARGUMENT;
   return gw_linear_impl(desc, T, a_codes, a_scale, u, w_codes, w_scale, l2b, bias_f32, nullptr,
                         Y32, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The operators beside the layer (include/hq_ops.h)
+extern "C" {
+
+hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
+                       const float* a_scale, const float* a_mean, const int8_t* w_codes,
+                       const float* w_scale, const float* colsum, const float* bias_f32,
+                       const hq_epilogue* epilogue, uint16_t* Y, int32_t* acc_debug,
+                       hq_stream_t stream) {
+  hq_status s = check_linear_args(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum,
+                                  bias_f32, Y, acc_debug);
+  if (s == HQ_OK) s = check_epilogue(epilogue, T, desc->N, Y);
+  if (s != HQ_OK || T == 0) return s;
+  if (T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
+  return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
+                     plain_epilogue(epilogue) ? nullptr : epilogue, Y, acc_debug, stream);
+}
+
+hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, const uint16_t* W,
+                   const uint16_t* bias, const hq_epilogue* epilogue, uint16_t* Y,
+                   hq_stream_t stream) {
+  if (desc == nullptr || T < 0 || desc->K <= 0 || desc->N <= 0) return HQ_ERR_INVALID_ARGUMENT;
+  const int K = desc->K, N = desc->N;
+  if (K % 8 != 0 || N % 8 != 0 || K > (1 << 20) || T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
+  hq_status s = check_epilogue(epilogue, T, N, Y);
+  if (s != HQ_OK || T == 0) return s;
+  if (X == nullptr || W == nullptr || Y == nullptr) return HQ_ERR_INVALID_ARGUMENT;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || (bias && !aligned16(bias)))
+    return HQ_ERR_MISALIGNED;
+  const uint64_t ybytes = uint64_t(T) * uint64_t(N) * 2u;
+  if (overlaps(Y, ybytes, X, uint64_t(T) * uint64_t(K) * 2u) ||
+      overlaps(Y, ybytes, W, uint64_t(N) * uint64_t(K) * 2u) ||
+      overlaps(Y, ybytes, bias, uint64_t(N) * 2u))
+    return HQ_ERR_INVALID_ARGUMENT;
+  DeviceState* dev;
+  s = device_state(&dev);
+  if (s != HQ_OK) return s;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int KB = 2 * K;  // bytes per row of X and W
+  const GemmChoice gc = choose_gemm(T, N, KB, dev->sm_count, pair_clusters(dev), HQ_GEMM_AUTO, 0,
+                                    false);
+  const int bn = gc.pair ? 256 : gc.bn;
+  CUtensorMap ta, tb, ty, tr;
+  if ((s = encode_kmajor_i8(&ta, X, T, KB, 128)) != HQ_OK) return s;
+  if ((s = encode_kmajor_i8(&tb, W, N, KB, gc.pair ? 128 : bn)) != HQ_OK) return s;
+  if ((s = encode_out_bf16(&ty, Y, T, N)) != HQ_OK) return s;
+  GemmEpParams p;
+  std::memset(&p, 0, sizeof(p));
+  const void* tmap_r = nullptr;
+  if (epilogue != nullptr) {
+    p.act = epilogue->act;
+    p.gate = epilogue->gate;
+    p.gate_rows = epilogue->gate_rows;
+    if (epilogue->residual != nullptr) {
+      if ((s = encode_out_bf16(&tr, epilogue->residual, T, N)) != HQ_OK) return s;
+      tmap_r = &tr;
+    }
+  }
+  p.bias16 = bias;
+  p.Y = Y;
+  p.T = T;
+  p.N = N;
+  p.K = KB;
+  p.group_m = kGroupM;
+  p.err = dev->err;
+  p.wait_ns = wait_ns();
+  const int bm = gc.pair ? 256 : 128;
+  const int64_t mt = (T + bm - 1) / bm, nt = (N + bn - 1) / bn;
+  if (mt * nt >= (int64_t(1) << 31) - 1024) return HQ_ERR_UNSUPPORTED;
+  p.num_m_tiles = int(mt);
+  p.num_n_tiles = int(nt);
+  if (gc.pair) {
+    const int clusters = int(mt * nt < dev->pair_clusters ? mt * nt : dev->pair_clusters);
+    return from_cuda(launch_gemm_pair_ep(true, &ta, &tb, &ty, tmap_r, p, clusters, st));
+  }
+  const int grid = int(mt * nt < dev->sm_count ? mt * nt : dev->sm_count);
+  return from_cuda(launch_gemm_ep(true, bn, 0, false, &ta, &tb, &ty, tmap_r, p, grid, st));
+}
+
+}  // extern "C"
+
+namespace {
+hq_status check_gn_desc(const hq_group_norm_desc* d) {
+  if (d == nullptr || d->C <= 0 || d->groups <= 0 || !known_act(d->act) || !(d->eps >= 0.0f) ||
+      !std::isfinite(d->eps))
+    return HQ_ERR_INVALID_ARGUMENT;
+  if (d->C > 8192 || d->C % d->groups != 0) return HQ_ERR_UNSUPPORTED;
+  return HQ_OK;
+}
+
+// The workspace depends on the current device's SM count where there is one.
+int sms_or_default() {
+  DeviceState* dev;
+  return device_state(&dev) == HQ_OK ? dev->sm_count : 148;
+}
+}  // namespace
+
+extern "C" {
+
+size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, int64_t S) {
+  if (check_gn_desc(desc) != HQ_OK || B <= 0 || S <= 0) return 0;
+  return size_t(B) * size_t(gn_chunks(B, S, desc->C, sms_or_default())) * size_t(desc->groups) *
+         sizeof(float2);
+}
+
+hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64_t B, int64_t S,
+                        const uint16_t* gamma, const uint16_t* beta, uint16_t* Y, void* workspace,
+                        size_t workspace_bytes, hq_stream_t stream) {
+  hq_status s = check_gn_desc(desc);
+  if (s != HQ_OK) return s;
+  if (B < 0 || S < 0) return HQ_ERR_INVALID_ARGUMENT;
+  if (B == 0 || S == 0) return HQ_OK;
+  if (X == nullptr || Y == nullptr) return HQ_ERR_INVALID_ARGUMENT;
+  if (!aligned16(X) || !aligned16(Y) || (gamma && !aligned16(gamma)) ||
+      (beta && !aligned16(beta)))
+    return HQ_ERR_MISALIGNED;
+  // images and rows are counted in 31 bits, elements in 62
+  if (B >= (int64_t(1) << 31) || S >= (int64_t(1) << 31)) return HQ_ERR_UNSUPPORTED;
+  const uint64_t bytes = uint64_t(B) * uint64_t(S) * uint64_t(desc->C) * 2u;
+  const uint64_t cb = uint64_t(desc->C) * 2u;
+  if ((X != Y && overlaps(Y, bytes, X, bytes)) || overlaps(Y, bytes, gamma, cb) ||
+      overlaps(Y, bytes, beta, cb))
+    return HQ_ERR_INVALID_ARGUMENT;
+  DeviceState* dev;
+  s = device_state(&dev);
+  if (s != HQ_OK) return s;
+  const size_t need = hq_group_norm_workspace_bytes(desc, B, S);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return HQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return HQ_ERR_MISALIGNED;
+    if (overlaps(workspace, need, X, bytes) || overlaps(workspace, need, Y, bytes))
+      return HQ_ERR_INVALID_ARGUMENT;
+  }
+  GnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.X = X;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.Y = Y;
+  p.part = static_cast<float2*>(workspace);
+  p.B = B;
+  p.S = S;
+  p.C = desc->C;
+  p.G = desc->groups;
+  p.act = desc->act;
+  p.eps = desc->eps;
+  p.P = gn_chunks(B, S, desc->C, dev->sm_count);
+  p.rows_p = (S + p.P - 1) / p.P;
+  if (B * p.P >= (int64_t(1) << 31)) return HQ_ERR_UNSUPPORTED;
+  return from_cuda(launch_group_norm(p, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

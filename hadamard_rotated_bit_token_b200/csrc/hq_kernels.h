@@ -123,6 +123,29 @@ cudaError_t gemm_pair_max_clusters(int* clusters);
 size_t gemm_pair_smem_bytes();
 int gemm_pair_stages();
 
+// The GEMM with an activation, a gate and a residual in its epilogue
+// (hq_gemm_ep.cu): Y = bf16(R + g * act(z)), z what the plain epilogue rounds.
+struct GemmEpParams : GemmParams {
+  int act;                // HQ_ACT_*
+  const uint16_t* gate;   // bf16 [ceil(T / gate_rows), N] or null
+  int64_t gate_rows;      // rows of Y per row of the gate
+  const uint16_t* bias16; // bf16 operands: bf16 bias [N] or null (p.bias is null)
+};
+
+// As launch_gemm / launch_gemm_pair.  tmap_r: the residual's map, laid out as
+// tmap_y, or null.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as bytes
+// (p.K = bytes per row; logo 0, not packed).
+cudaError_t launch_gemm_ep(bool bf16, int bn, int logo, bool packed_a, const void* tmap_a,
+                           const void* tmap_b, const void* tmap_y, const void* tmap_r,
+                           const GemmEpParams& p, int grid, cudaStream_t st);
+cudaError_t launch_gemm_pair_ep(bool bf16, const void* tmap_a, const void* tmap_b,
+                                const void* tmap_y, const void* tmap_r, const GemmEpParams& p,
+                                int clusters, cudaStream_t st);
+// The packed-code kernels of launch_gemm_ep (hq_gemm_ep_pk.cu).
+cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* tmap_a, const void* tmap_b,
+                                  const void* tmap_y, const void* tmap_r, const GemmEpParams& p,
+                                  int grid, cudaStream_t st);
+
 // MMA-only loop (the int8 tensor-core ceiling): `ctas` CTAs (an even number
 // of them in clusters of two when pair), each issuing k_blocks x 4 MMAs of
 // 128 x 256 x 32 (pair: 256 x 256 x 32 per cluster, half per CTA).
@@ -201,5 +224,25 @@ cudaError_t launch_gw_gemm(const void* tmaps, const GwGemmParams& p, int grid, c
 size_t gw_gemm_smem_bytes();
 int gw_gemm_threads();
 int gw_gemm_bn();  // output tile width (the B, s_w and l2 boxes have this many rows)
+
+// ---------------------------------------------------------------------------
+// Group norm with an activation, channels last: hq_norm.cu.
+struct GnParams {
+  const uint16_t* X;      // bf16 [B,S,C]
+  const uint16_t* gamma;  // bf16 [C] or null (1)
+  const uint16_t* beta;   // bf16 [C] or null (0)
+  uint16_t* Y;            // bf16 [B,S,C]
+  float2* part;           // [B][P][G] (mean, sum of squared deviations)
+  int64_t B, S;
+  int C, G;
+  int act;
+  float eps;
+  int P;                  // row chunks per image of the statistics kernel
+  int64_t rows_p;         // rows per chunk
+};
+
+// Row chunks per image (GnParams.P) on a device with `sms` SMs.
+int gn_chunks(int64_t B, int64_t S, int C, int sms);
+cudaError_t launch_group_norm(const GnParams& p, int sms, cudaStream_t st);
 
 }  // namespace hq

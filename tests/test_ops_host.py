@@ -1,0 +1,133 @@
+"""Host-side checks of the operators beside the layer (include/hq_ops.h), no
+GPU needed: every refusal of the C ABI happens before the device is touched,
+and the Python binding refuses tensors that do not fit."""
+import ctypes
+
+import pytest
+
+FAKE = 0x10000      # aligned, never dereferenced: every call below is refused or a no-op
+FAR = 0x100000000   # a second buffer far from FAKE
+OK, INVALID, UNSUPPORTED, MISALIGNED = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def hq():
+    from hadamard_rotated_bit_token_b200 import build as hq_build
+    hq_build.build()
+    import hadamard_rotated_bit_token_b200 as hq_mod
+    hq_mod.load_library()
+    return hq_mod
+
+
+def _ep(hq, act=0, residual=None, gate=None, gate_rows=0):
+    e = hq.Epilogue(act)
+    e._residual, e._gate, e.gate_rows = residual, gate, gate_rows
+    return ctypes.byref(e)
+
+
+def test_dense_refusals(hq):
+    lib = hq.load_library()
+
+    def call(K=64, N=64, T=4, X=FAKE, W=2 * FAR, b=None, ep=None, Y=FAR, desc=True):
+        d = ctypes.byref(hq.DenseDesc(K, N)) if desc else None
+        return lib.hq_dense(d, X, T, W, b, ep, Y, None)
+
+    assert call(desc=False) == INVALID
+    assert call(K=0) == INVALID and call(N=-8) == INVALID and call(T=-1) == INVALID
+    assert call(K=60) == UNSUPPORTED and call(N=20) == UNSUPPORTED
+    assert call(K=(1 << 20) + 8) == UNSUPPORTED and call(T=2 ** 31 - 255) == UNSUPPORTED
+    for name in ("X", "W", "Y"):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: FAKE + 8}) == MISALIGNED
+    assert call(b=FAKE + 4) == MISALIGNED
+    # Y over an input
+    assert call(Y=FAKE) == INVALID
+    assert call(Y=FAKE + 64 * 2) == INVALID
+    assert call(Y=2 * FAR - 16) == INVALID
+    assert call(b=FAR + 16) == INVALID
+    # the epilogue
+    assert call(ep=_ep(hq, act=5)) == INVALID and call(ep=_ep(hq, act=-1)) == INVALID
+    assert call(ep=_ep(hq, gate=3 * FAR)) == INVALID               # gate_rows 0
+    assert call(ep=_ep(hq, gate=3 * FAR, gate_rows=-2)) == INVALID
+    assert call(ep=_ep(hq, residual=3 * FAR + 8)) == MISALIGNED
+    assert call(ep=_ep(hq, gate=3 * FAR + 2, gate_rows=1)) == MISALIGNED
+    assert call(ep=_ep(hq, residual=FAR + 128)) == INVALID         # partly Y
+    assert call(ep=_ep(hq, gate=FAR + 16, gate_rows=4)) == INVALID  # the gate inside Y
+    # nothing to do: no pointer is looked at, but the description is
+    assert call(T=0, X=None, W=None, Y=None) == OK
+    assert call(T=0, ep=_ep(hq, act=9)) == INVALID
+
+
+def test_linear_ep_refusals(hq):
+    lib = hq.load_library()
+    D = hq.LayerDesc
+
+    def call(desc, T=8, a=FAKE, sx=FAKE, m=None, w=FAKE, sw=FAKE, cs=None, b=None, ep=None, y=FAR):
+        return lib.hq_linear_ep(None if desc is None else ctypes.byref(desc), T, a, sx, m, w, sw,
+                                cs, b, ep, y, None, None)
+
+    d = D(1024, 64, 1024)
+    assert call(None) == INVALID and call(d, T=-1) == INVALID and call(d, a=None) == INVALID
+    assert call(D(1000, 64, 8)) == UNSUPPORTED and call(D(1024, 24, 1024)) == UNSUPPORTED
+    assert call(d, y=FAR + 2) == MISALIGNED and call(d, m=FAKE) == INVALID
+    assert call(d, ep=_ep(hq, act=7)) == INVALID
+    assert call(d, ep=_ep(hq, gate=3 * FAR)) == INVALID
+    assert call(d, ep=_ep(hq, residual=FAR + 64)) == INVALID
+    assert call(d, ep=_ep(hq, residual=3 * FAR + 4)) == MISALIGNED
+    assert call(d, T=2 ** 31 - 255, ep=_ep(hq, act=1)) == UNSUPPORTED
+    assert call(d, T=0, a=None, ep=_ep(hq, act=1)) == OK
+
+
+def test_group_norm_refusals(hq):
+    lib = hq.load_library()
+
+    def call(C=64, G=8, act=0, eps=1e-5, B=2, S=16, X=FAKE, ga=None, be=None, Y=FAR, ws=None,
+             nws=0, desc=True):
+        d = ctypes.byref(hq.GroupNormDesc(C, G, act, eps)) if desc else None
+        return lib.hq_group_norm(d, X, B, S, ga, be, Y, ws, nws, None)
+
+    assert call(desc=False) == INVALID
+    assert call(C=0) == INVALID and call(G=0) == INVALID and call(act=5) == INVALID
+    assert call(eps=-1.0) == INVALID and call(eps=float("nan")) == INVALID
+    assert call(eps=float("inf")) == INVALID
+    assert call(G=7) == UNSUPPORTED and call(C=8200, G=8) == UNSUPPORTED
+    assert call(B=-1) == INVALID and call(S=-1) == INVALID
+    assert call(X=None) == INVALID and call(Y=None) == INVALID
+    assert call(X=FAKE + 2) == MISALIGNED and call(Y=FAR + 8) == MISALIGNED
+    assert call(ga=FAKE + 2) == MISALIGNED and call(be=FAKE + 4) == MISALIGNED
+    assert call(Y=FAKE + 16) == INVALID and call(X=FAR - 32) == INVALID
+    assert call(ga=FAR + 16) == INVALID and call(be=FAR + 32) == INVALID
+    assert call(B=2 ** 31) == UNSUPPORTED and call(S=2 ** 31) == UNSUPPORTED
+    assert call(B=0, X=None, Y=None) == OK and call(S=0, X=None) == OK
+    assert lib.hq_group_norm_workspace_bytes(None, 1, 1) == 0
+    assert hq.hq_group_norm_workspace_bytes(hq.GroupNormDesc(64, 7), 1, 1) == 0
+    assert hq.hq_group_norm_workspace_bytes(hq.GroupNormDesc(64, 8), 0, 5) == 0
+
+
+def test_binding_refusals(hq):
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device memory"):
+        hq.hq_dense(hq.DenseDesc(64, 64), t, t, None, None, t)
+    with pytest.raises(ValueError, match="device memory"):
+        hq.hq_group_norm(hq.GroupNormDesc(64, 8), t, None, None, t)
+    with pytest.raises(ValueError, match="shape"):
+        hq.hq_group_norm(hq.GroupNormDesc(32, 8), t, None, None, t)
+    with pytest.raises(ValueError, match="device memory"):
+        hq.hq_linear_ep(hq.LayerDesc(64, 64, 64), t, None, None, t, t, t, t, None, t)
+    with pytest.raises(ValueError, match="gate_rows"):
+        hq.Epilogue(0, gate=t)
+    with pytest.raises(ValueError, match="device memory"):
+        hq.Epilogue(0, residual=t)
+
+
+def test_block_refusals(hq):
+    class Layer:
+        desc = hq.LayerDesc(64, 32, 64)
+    norm = hq.GroupNorm(64, 8)
+    with pytest.raises(ValueError, match="channels"):
+        hq.PointwiseBlock(hq.GroupNorm(32, 8), Layer())
+    with pytest.raises(ValueError, match="outputs"):
+        hq.PointwiseBlock(norm, Layer(), residual=True)
+    with pytest.raises(ValueError, match="HadamardQuantLinear"):
+        hq.PointwiseBlock(norm, Layer(), act=hq.HQ_ACT_SILU)
