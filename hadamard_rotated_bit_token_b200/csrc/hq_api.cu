@@ -1699,8 +1699,16 @@ extern "C" {
 
 size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, int64_t S) {
   if (check_gn_desc(desc) != HQ_OK || B <= 0 || S <= 0) return 0;
-  return size_t(B) * size_t(gn_chunks(B, S, desc->C, sms_or_default())) * size_t(desc->groups) *
-         sizeof(float2);
+  if (B >= (int64_t(1) << 31) || S >= (int64_t(1) << 31)) return 0;  // refused by the call
+  GnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.B = B;
+  p.S = S;
+  p.C = desc->C;
+  p.G = desc->groups;
+  int vec;
+  gn_plan(&p, &vec, sms_or_default());
+  return size_t(B) * size_t(p.P) * size_t(p.G) * sizeof(float2);
 }
 
 hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64_t B, int64_t S,
@@ -1724,30 +1732,27 @@ hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64
   DeviceState* dev;
   s = device_state(&dev);
   if (s != HQ_OK) return s;
-  const size_t need = hq_group_norm_workspace_bytes(desc, B, S);
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need) return HQ_ERR_INVALID_ARGUMENT;
-    if (!aligned16(workspace)) return HQ_ERR_MISALIGNED;
-    if (overlaps(workspace, need, X, bytes) || overlaps(workspace, need, Y, bytes))
-      return HQ_ERR_INVALID_ARGUMENT;
-  }
   GnParams p;
   std::memset(&p, 0, sizeof(p));
   p.X = X;
   p.gamma = gamma;
   p.beta = beta;
   p.Y = Y;
-  p.part = static_cast<float2*>(workspace);
   p.B = B;
   p.S = S;
   p.C = desc->C;
   p.G = desc->groups;
   p.act = desc->act;
   p.eps = desc->eps;
-  p.P = gn_chunks(B, S, desc->C, dev->sm_count);
-  p.rows_p = (S + p.P - 1) / p.P;
-  if (B * p.P >= (int64_t(1) << 31)) return HQ_ERR_UNSUPPORTED;
-  return from_cuda(launch_group_norm(p, dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+  int vec;
+  gn_plan(&p, &vec, dev->sm_count);
+  const size_t need = size_t(B) * size_t(p.P) * size_t(p.G) * sizeof(float2);
+  if (workspace == nullptr || workspace_bytes < need) return HQ_ERR_INVALID_ARGUMENT;
+  if (!aligned16(workspace)) return HQ_ERR_MISALIGNED;
+  if (overlaps(workspace, need, X, bytes) || overlaps(workspace, need, Y, bytes))
+    return HQ_ERR_INVALID_ARGUMENT;
+  p.part = static_cast<float2*>(workspace);
+  return from_cuda(launch_group_norm(vec, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -232,17 +232,30 @@ struct GnParams {
   const uint16_t* gamma;  // bf16 [C] or null (1)
   const uint16_t* beta;   // bf16 [C] or null (0)
   uint16_t* Y;            // bf16 [B,S,C]
-  float2* part;           // [B][P][G] (mean, sum of squared deviations)
   int64_t B, S;
   int C, G;
   int act;
   float eps;
-  int P;                  // row chunks per image of the statistics kernel
-  int64_t rows_p;         // rows per chunk
+  float2* part;           // [B][P][G] (mean, sum of squared deviations)
+  // the rest is gn_plan's: chunks of rows_p rows (the last rows_last), P an image
+  int cpg;                // channels per group
+  int P, rows_p, rows_last;
+  float n_full, n_last;   // values of a group in a chunk
+  float inv_n_full, inv_n_last, inv_n;  // reciprocals: of those and of an image's
+  // statistics: passes of gs groups = nv vectors, RP rows side by side, each
+  // thread q rows or one more; kk threads a channel and `lanes` a group merge
+  int gs, nv, RP, q_full, q_last;
+  int kk, lanes, log_lanes;
+  // normalization: nva vectors, RPa rows side by side, qa rows a thread or one
+  // more; ka threads and lanes_a lanes a group merge the chunks
+  int nva, RPa, qa_full, qa_last, ka, lanes_a, log_lanes_a;
+  // ceil(2^32 / d) for divisions by nv, a pass's channels, nva, G and cpg (0: d = 1)
+  unsigned magic_nv, magic_m, magic_nva, magic_g, magic_cpg;
 };
 
-// Row chunks per image (GnParams.P) on a device with `sms` SMs.
-int gn_chunks(int64_t B, int64_t S, int C, int sms);
-cudaError_t launch_group_norm(const GnParams& p, int sms, cudaStream_t st);
+// Fills in the plan of p (B, S, C and G set) and the channels per load (host
+// only).
+void gn_plan(GnParams* p, int* vec, int sms);
+cudaError_t launch_group_norm(int vec, const GnParams& p, cudaStream_t st);
 
 }  // namespace hq

@@ -3,15 +3,25 @@
 //   y = act((x - mean) / sqrt(var + eps) * gamma_c + beta_c)
 //
 // with mean and variance over the S pixels and C / G channels of an image's
-// group.  Two launches: gn_stats_kernel leaves each row chunk's (mean, sum of
-// squared deviations) per group in the workspace, gn_apply_kernel merges the
-// chunks' statistics and normalizes.
+// group.  Two launches: gn_stats_kernel leaves (mean, M2 = sum of squared
+// deviations) of every row chunk and group in the workspace; gn_apply_kernel,
+// launched as its programmatic dependent (it starts while the first drains,
+// loads its first rows, and waits), merges the chunks' statistics, normalizes
+// and writes.  X is read twice, the second time from L2 as far as the tensor
+// fits there.
 //
-// Statistics never subtract large sums: a thread accumulates deviations from
-// its own first value of the channel, turns them into (mean, M2), and parts i
-// of n_i values merge as  mean = mean_0 + sum n_i (mean_i - mean_0) / n,
-// M2 = sum M2_i + n_i (mean_i - mean)^2  (equal values: mean exactly theirs).
+// Statistics never subtract large sums.  Parts i of n_i values with mean m_i
+// and M2 q_i merge around the first part's mean m_0:
+//   s1 = sum n_i (m_i - m_0),  s2 = sum q_i + n_i (m_i - m_0)^2,
+//   mean = m_0 + s1 / n,  M2 = s2 - s1^2 / n.
+// Part 0 itself adds n_0 (m_0 - mean)^2 to M2, so (m_0 - mean)^2 n <= M2 n / n_0
+// and the subtraction costs at most a factor n / n_0, the number of parts,
+// whatever the data.  A thread's values of one channel merge the same way
+// around the first of them.  Orders depend on sizes alone; equal values give
+// exactly their mean and M2 = 0.
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "hq_act.cuh"
 #include "hq_device.cuh"
@@ -21,8 +31,12 @@ namespace hq {
 
 namespace {
 
-constexpr int kGnThreads = 256;
+constexpr int kGnThreads = 512;
+// Per-thread parts: value i of thread t at part[i * kPartLd + t], so a warp
+// stores without bank conflicts (and reads nearly so: the odd pitch).
+constexpr int kPartLd = kGnThreads + 1;
 
+// VEC bf16 values of consecutive channels, loaded at once.
 template <int VEC>
 struct Vec;
 template <>
@@ -35,212 +49,546 @@ template <>
 struct Vec<1> { typedef uint16_t T; };
 
 template <int VEC>
-__device__ __forceinline__ void load_vec(const uint16_t* p, float (&v)[VEC]) {
-  const typename Vec<VEC>::T raw = *reinterpret_cast<const typename Vec<VEC>::T*>(p);
-  const uint16_t* h = reinterpret_cast<const uint16_t*>(&raw);
+__device__ __forceinline__ void unpack_vec(const typename Vec<VEC>::T& raw, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = __uint_as_float(uint32_t(raw) << 16);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(uint32_t(h[i]) << 16);
+    for (int i = 0; i < VEC / 2; ++i) {
+      const f2 p = unpack_bf16x2(w[i]);
+      v[2 * i] = p.x;
+      v[2 * i + 1] = p.y;
+    }
+  }
 }
 
+// A thread's running sums for VEC channels around each channel's first value.
 template <int VEC>
-__device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC]) {
-  typename Vec<VEC>::T raw;
-  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(&raw);
+struct ThreadStats {
+  float piv[VEC], s1[VEC], s2[VEC];
+  __device__ __forceinline__ void start(const typename Vec<VEC>::T& raw) {
+    unpack_vec<VEC>(raw, piv);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) h[i] = __float2bfloat16_rn(v[i]);
-  *reinterpret_cast<typename Vec<VEC>::T*>(p) = raw;
+    for (int i = 0; i < VEC; ++i) s1[i] = s2[i] = 0.0f;
+  }
+  __device__ __forceinline__ void add(const typename Vec<VEC>::T& raw) {
+    float v[VEC];
+    unpack_vec<VEC>(raw, v);
+    if constexpr (VEC == 1) {
+      const float d = v[0] - piv[0];
+      s1[0] += d;
+      s2[0] = fmaf(d, d, s2[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 2) {
+        const f2 d = sub2(pk(v[i], v[i + 1]), pk(piv[i], piv[i + 1]));
+        const f2 a = add2(pk(s1[i], s1[i + 1]), d);
+        const f2 b = fma2(d, d, pk(s2[i], s2[i + 1]));
+        s1[i] = a.x, s1[i + 1] = a.y;
+        s2[i] = b.x, s2[i + 1] = b.y;
+      }
+    }
+  }
+  // (mean, M2) of n values a channel -> this thread's column of `part`
+  __device__ __forceinline__ void finish(int n, float2* part) const {
+    const float inv = rcp_approx(float(n));
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float m = s1[i] * inv;
+      part[i * kPartLd + threadIdx.x] = make_float2(piv[i] + m, s2[i] - s1[i] * m);
+    }
+  }
+};
+
+// Merging around `ref`: add() parts, reduce the two sums, finish().
+struct Merge {
+  float ref, s1, s2;
+  __device__ __forceinline__ void add(float n, float2 part) {
+    const float d = part.x - ref;
+    s1 = fmaf(n, d, s1);
+    s2 += fmaf(n * d, d, part.y);
+  }
+  __device__ __forceinline__ float2 finish(float inv_n) const {
+    const float m = s1 * inv_n;
+    return make_float2(ref + m, s2 - s1 * m);
+  }
+};
+
+__device__ __forceinline__ float2 mean_rstd(float2 stat, float inv_n, float eps) {
+  // the rounding of M2's subtraction can leave a tiny negative value
+  const float var = stat.y * inv_n;
+  return make_float2(stat.x, rsqrtf((var < 0.0f ? 0.0f : var) + eps));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// x / d for x < 2^16, with magic = ceil(2^32 / d) (0 for d = 1)
+__device__ __forceinline__ int div_small(int x, unsigned magic) {
+  return magic ? int(__umulhi(unsigned(x), magic)) : x;
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p, int i, float none) {
+  return p ? __uint_as_float(uint32_t(p[i]) << 16) : none;
+}
+
+// The normalization of VEC consecutive channels, and the activation.
+// Coefficients of a channel: mean, a = rstd gamma, beta.
+template <int VEC>
+struct Normalize {
+  float mean[VEC], a[VEC], b[VEC];
+  // coef: [3][ld] in shared memory, this thread's channels from c on
+  __device__ __forceinline__ void load(const float* coef, int ld, int c) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int i = 0; i < VEC; ++i) {
+      mean[i] = coef[c + i];
+      a[i] = coef[ld + c + i];
+      b[i] = coef[2 * ld + c + i];
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ typename Vec<VEC>::T apply(const typename Vec<VEC>::T& raw) const {
+    float v[VEC];
+    unpack_vec<VEC>(raw, v);
+    constexpr int NP = (VEC + 1) / 2;
+    f2 z[NP];
+    if constexpr (VEC == 1) {
+      z[0] = pk(fmaf(v[0] - mean[0], a[0], b[0]), 0.0f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        z[i] = fma2(sub2(pk(v[2 * i], v[2 * i + 1]), pk(mean[2 * i], mean[2 * i + 1])),
+                    pk(a[2 * i], a[2 * i + 1]), pk(b[2 * i], b[2 * i + 1]));
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) z[i] = act_one<ACT>(z[i]);
+    typename Vec<VEC>::T out;
+    if constexpr (VEC == 1) {
+      out = uint16_t(pack_bf16x2(z[0].x, 0.0f) & 0xFFFFu);
+    } else {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&out);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) w[i] = pack_bf16x2(z[i].x, z[i].y);
+    }
+    return out;
+  }
+};
+
+// The previous kernel of the stream has finished and its writes are visible.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The next kernel of the stream may start once every CTA has come here.
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The CTA's per-thread parts -> (mean, M2) of gs groups in out[0 .. gs).
+// Thread t = rp * nv + cv (rp < used) holds VEC of the M = nv * VEC channels,
+// with w + 1 values a channel where rp < rem and w elsewhere; channel c has
+// v_hi values in all where c < vsplit, else v_lo; a group has cpg = M / gs
+// channels.  kk threads a channel, then L lanes a group (p.kk, p.lanes; both
+// chosen on the host).  sums: [max(kGnThreads, M)] scratch.  All threads call
+// it; the parts are synchronized on entry, out is not on exit.
+template <int VEC>
+__device__ __forceinline__ void block_group_stats(const GnParams& p, const float2* part,
+                                                  float2* sums, int used, int nv, int cpg,
+                                                  int gs, float inv_n, int rem, float w,
+                                                  int vsplit, float v_hi, float v_lo,
+                                                  float2* out) {
+  const int M = nv * VEC;
+  const int k = p.kk == 1 ? 0 : div_small(int(threadIdx.x), p.magic_m);
+  if (k < p.kk) {
+    for (int c = int(threadIdx.x) - k * M; c < M; c += kGnThreads) {
+      const float2* q = part + (c % VEC) * kPartLd + c / VEC;
+      Merge m{q[0].x, 0.0f, 0.0f};
+      const int stride = p.kk * nv;
+      q += k * nv;
+#pragma unroll 4
+      for (int rp = k; rp < used; rp += p.kk, q += stride) m.add(rp < rem ? w + 1.0f : w, *q);
+      sums[k * M + c] = make_float2(m.s1, m.s2);
+    }
+  }
+  __syncthreads();
+  const int L = p.lanes;
+  const int l = int(threadIdx.x) & (L - 1);
+  const float i_hi = rcp_approx(v_hi), i_lo = v_lo > 0.0f ? rcp_approx(v_lo) : 0.0f;
+  const int per = kGnThreads >> p.log_lanes;  // groups at a time
+  for (int g0 = 0; g0 < gs; g0 += per) {
+    const int g = g0 + (int(threadIdx.x) >> p.log_lanes);
+    const int cg = min(g, gs - 1) * cpg;
+    Merge m{part[(cg % VEC) * kPartLd + cg / VEC].x, 0.0f, 0.0f};
+    for (int c = cg + l; c < cg + cpg; c += L) {
+      float s1 = 0.0f, s2 = 0.0f;
+      for (int j = 0; j < p.kk; ++j) {
+        const float2 v = sums[j * M + c];
+        s1 += v.x;
+        s2 += v.y;
+      }
+      const bool hi = c < vsplit;
+      const float mc = s1 * (hi ? i_hi : i_lo);
+      m.add(hi ? v_hi : v_lo,
+            make_float2(part[(c % VEC) * kPartLd + c / VEC].x + mc, s2 - s1 * mc));
+    }
+    for (int o = L >> 1; o > 0; o >>= 1) {
+      m.s1 += __shfl_xor_sync(0xffffffffu, m.s1, o);
+      m.s2 += __shfl_xor_sync(0xffffffffu, m.s2, o);
+    }
+    if (l == 0 && g < gs) out[g] = m.finish(inv_n);
+  }
 }
 
 }  // namespace
 
-// One CTA: a chunk of rows of one image.  Threads sit rp x cv over rows
-// and channel vectors; the per-channel parts of the rp threads merge in shared
-// memory, then a warp per group merges the group's channels.
+// The grid is (P, B) with images beyond 65535 along z.
+__device__ __forceinline__ int64_t image_of_block() {
+  return int64_t(blockIdx.z) * 65535 + blockIdx.y;
+}
+
+// One CTA: a chunk of rows of one image.  Thread rp * nv + cv walks rows rp,
+// rp + RP, ... of vector column cv with eight loads in flight.
 template <int VEC>
-__global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(const GnParams p) {
+__global__ void __launch_bounds__(kGnThreads, 2) gn_stats_kernel(const GnParams p) {
   extern __shared__ float2 sm[];
-  float2* chan = sm;         // [C] (mean, M2) over the chunk's rows
-  float2* part = sm + p.C;   // [kGnThreads * VEC] per thread and channel
-  const int64_t b = blockIdx.x / unsigned(p.P);
-  const int chunk = int(blockIdx.x % unsigned(p.P));
-  const int64_t r0 = int64_t(chunk) * p.rows_p;
-  const int64_t r1 = r0 + p.rows_p < p.S ? r0 + p.rows_p : p.S;
-  const int rows = int(r1 - r0);
+  float2* part = sm;                   // [VEC][kPartLd]
+  float2* sums = sm + VEC * kPartLd;   // [max(kGnThreads, channels of a pass)]
+  let_next_kernel_start();
+  const int64_t b = image_of_block();
+  if (b >= p.B) return;
+  const int chunk = int(blockIdx.x);
+  const bool last = chunk == p.P - 1;
+  const int rows = last ? p.rows_last : p.rows_p;
+  const float inv_n = last ? p.inv_n_last : p.inv_n_full;
+  const uint16_t* base = p.X + (b * p.S + int64_t(chunk) * p.rows_p) * p.C;
+  float2* outp = p.part + (b * p.P + chunk) * p.G;
+  typedef typename Vec<VEC>::T V;
+  const int nv = p.nv, RP = p.RP;
+  // passes over slices of p.gs whole groups, at most kGnThreads vectors a row;
+  // a single group may be wider: its row is then walked by all threads
+  for (int g0 = 0; g0 < p.G; g0 += p.gs) {
+    const uint16_t* xs = base + g0 * p.cpg;
+    if (nv <= kGnThreads) {
+      const int rp = div_small(int(threadIdx.x), p.magic_nv), cv = int(threadIdx.x) - rp * nv;
+      const int q = last ? p.q_last : p.q_full, rem = rows - q * RP;
+      if (rp < RP && rp < rows) {
+        const int step = RP * p.C;
+        const uint16_t* x = xs + rp * p.C + cv * VEC;
+        const int cnt = rp < rem ? q + 1 : q;
+        ThreadStats<VEC> ts;
+        ts.start(*reinterpret_cast<const V*>(x));
+        int i = 0;
+        for (; i + 8 <= cnt; i += 8) {
+          V raw[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ts.add(raw[j]);
+          x += 8 * step;
+        }
+        for (; i + 2 <= cnt; i += 2) {
+          const V r1 = *reinterpret_cast<const V*>(x), r2 = *reinterpret_cast<const V*>(x + step);
+          ts.add(r1);
+          ts.add(r2);
+          x += 2 * step;
+        }
+        if (i < cnt) ts.add(*reinterpret_cast<const V*>(x));
+        ts.finish(cnt, part);
+      }
+      __syncthreads();
+      block_group_stats<VEC>(p, part, sums, min(RP, rows), nv, p.cpg, p.gs, inv_n, rem, float(q),
+                             nv * VEC, float(rows), 0.0f, outp + g0);
+    } else {
+      ThreadStats<VEC> ts;
+      ts.start(*reinterpret_cast<const V*>(xs + threadIdx.x * VEC));
+      for (int r = 0; r < rows; ++r, xs += p.C)
+        for (int cv = threadIdx.x; cv < nv; cv += kGnThreads)
+          ts.add(*reinterpret_cast<const V*>(xs + cv * VEC));
+      const int q = nv / kGnThreads, rem = nv % kGnThreads;
+      ts.finish(rows * (int(threadIdx.x) < rem ? q + 1 : q), part);
+      __syncthreads();
+      // as one row of kGnThreads vectors, each with the values of its thread
+      block_group_stats<VEC>(p, part, sums, 1, kGnThreads, kGnThreads * VEC, 1, inv_n, 0, 0.0f,
+                             rem * VEC, float(rows) * float(q + 1), float(rows) * float(q),
+                             outp + g0);
+    }
+    if (g0 + p.gs < p.G) __syncthreads();
+  }
+}
+
+// One CTA: a chunk of rows of one image, normalized with the merged
+// statistics.  Chunks run from the end, whose rows the statistics read last.
+template <int VEC>
+__global__ void __launch_bounds__(kGnThreads, 1) gn_apply_kernel(const GnParams p) {
+  extern __shared__ float2 sm[];
+  float2* stat = sm;                                 // [G] (mean, 1 / sqrt(var + eps))
+  float* coef = reinterpret_cast<float*>(sm + p.G);  // [3][C]
+  float2* sums = reinterpret_cast<float2*>(coef + 3 * p.C + (p.C & 1));  // [kGnThreads]
+  const int64_t b = p.B - 1 - image_of_block();
+  if (b < 0) return;
+  const int chunk = p.P - 1 - int(blockIdx.x);
+  const int rows = chunk == p.P - 1 ? p.rows_last : p.rows_p;
+  const int64_t base = (b * p.S + int64_t(chunk) * p.rows_p) * p.C;
   const int CV = p.C / VEC;
-  const uint16_t* base = p.X + (b * p.S + r0) * p.C;
-  for (int v0 = 0; v0 < CV; v0 += kGnThreads) {
-    const int nv = CV - v0 < kGnThreads ? CV - v0 : kGnThreads;  // vectors in this pass
-    const int RP = kGnThreads / nv;                              // rows side by side
-    const int rp = threadIdx.x / nv, cv = threadIdx.x % nv;
-    if (rp < RP && rp < rows) {
-      const uint16_t* x = base + int64_t(rp) * p.C + (v0 + cv) * VEC;
-      float piv[VEC], s1[VEC], s2[VEC];
-      load_vec<VEC>(x, piv);
+  typedef typename Vec<VEC>::T V;
+  // the first vector column's first rows and this thread's first channel's
+  // parameters, which do not depend on the statistics
+  constexpr int U = 4;
+  const int nva = p.nva, RPa = p.RPa;
+  const int rp = div_small(int(threadIdx.x), p.magic_nva), cv = int(threadIdx.x) - rp * nva;
+  const int step = RPa * p.C;
+  const uint16_t* x = p.X + base + rp * p.C + cv * VEC;
+  // rows of this thread
+  const int q = chunk == p.P - 1 ? p.qa_last : p.qa_full;
+  const int cnt = rp < rows - q * RPa ? q + 1 : q;
+  V raw[U];
+  if (rp < RPa) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s1[i] = s2[i] = 0.0f;
-      int n = 0;
-      for (int r = rp; r < rows; r += RP, x += int64_t(RP) * p.C, ++n) {
-        float v[VEC];
-        load_vec<VEC>(x, v);
+    for (int j = 0; j < U; ++j)
+      if (j < cnt) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+  }
+  float ga = 1.0f, be = 0.0f;
+  if (int(threadIdx.x) < p.C) {
+    ga = bf16_at(p.gamma, int(threadIdx.x), 1.0f);
+    be = bf16_at(p.beta, int(threadIdx.x), 0.0f);
+  }
+  wait_for_previous_kernel();
+  {
+    // ka threads a group share its P parts; thread k * G + g reads parts k,
+    // k + ka, ... of group g, neighbours neighbouring groups
+    const float2* parts = p.part + b * p.P * p.G;
+    const int k = p.ka == 1 ? 0 : div_small(int(threadIdx.x), p.magic_g);
+    if (k < p.ka) {
+      for (int g = int(threadIdx.x) - k * p.G; g < p.G; g += kGnThreads) {
+        Merge m{parts[g].x, 0.0f, 0.0f};
+        for (int i0 = k; i0 < p.P; i0 += 10 * p.ka) {
+          float2 v[10];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float d = v[i] - piv[i];
-          s1[i] += d;
-          s2[i] = fmaf(d, d, s2[i]);
+          for (int j = 0; j < 10; ++j)
+            if (i0 + j * p.ka < p.P) v[j] = parts[(i0 + j * p.ka) * p.G + g];
+#pragma unroll
+          for (int j = 0; j < 10; ++j)
+            if (i0 + j * p.ka < p.P)
+              m.add(i0 + j * p.ka == p.P - 1 ? p.n_last : p.n_full, v[j]);
+        }
+        if (k == 0) stat[g].x = m.ref;
+        if (p.ka == 1)
+          stat[g] = mean_rstd(m.finish(p.inv_n), p.inv_n, p.eps);
+        else
+          sums[k * p.G + g] = make_float2(m.s1, m.s2);
+      }
+    }
+    if (p.ka > 1) {
+      __syncthreads();
+      const int L = p.lanes_a;  // lanes a group: L * G <= kGnThreads
+      const int l = int(threadIdx.x) & (L - 1), g = int(threadIdx.x) >> p.log_lanes_a;
+      Merge m{0.0f, 0.0f, 0.0f};
+      if (g < p.G) {
+        m.ref = stat[g].x;
+        for (int j = l; j < p.ka; j += L) {
+          m.s1 += sums[j * p.G + g].x;
+          m.s2 += sums[j * p.G + g].y;
         }
       }
-      const float inv = 1.0f / float(n);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float m = s1[i] * inv;
-        part[rp * (nv * VEC) + cv * VEC + i] =
-            make_float2(piv[i] + m, fmaxf(fmaf(-s1[i], m, s2[i]), 0.0f));
+      for (int o = L >> 1; o > 0; o >>= 1) {
+        m.s1 += __shfl_xor_sync(0xffffffffu, m.s1, o);
+        m.s2 += __shfl_xor_sync(0xffffffffu, m.s2, o);
       }
+      // (the shuffles come after every lane's read of stat[g].x)
+      if (l == 0 && g < p.G) stat[g] = mean_rstd(m.finish(p.inv_n), p.inv_n, p.eps);
     }
-    __syncthreads();
-    const int used = RP < rows ? RP : rows;
-    for (int c = threadIdx.x; c < nv * VEC; c += kGnThreads) {
-      // rows of thread rp: ceil((rows - rp) / RP)
-      const float ref = part[c].x;
-      float mean = 0.0f;
-      for (int i = 1; i < used; ++i)
-        mean = fmaf(float((rows - i + RP - 1) / RP), part[i * (nv * VEC) + c].x - ref, mean);
-      mean = ref + mean / float(rows);
-      float m2 = 0.0f;
-      for (int i = 0; i < used; ++i) {
-        const float2 q = part[i * (nv * VEC) + c];
-        const float d = q.x - mean;
-        m2 += fmaf(float((rows - i + RP - 1) / RP) * d, d, q.y);
-      }
-      chan[v0 * VEC + c] = make_float2(mean, m2);
-    }
-    __syncthreads();
-  }
-  const int cpg = p.C / p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int g = warp; g < p.G; g += kGnThreads / 32) {
-    const float ref = chan[g * cpg].x;
-    float mean = 0.0f;
-    for (int c = lane; c < cpg; c += 32) mean += chan[g * cpg + c].x - ref;
-    mean = ref + warp_sum(mean) / float(cpg);
-    float m2 = 0.0f;
-    for (int c = lane; c < cpg; c += 32) {
-      const float2 q = chan[g * cpg + c];
-      const float d = q.x - mean;
-      m2 += fmaf(float(rows) * d, d, q.y);
-    }
-    m2 = warp_sum(m2);
-    if (lane == 0) p.part[(b * p.P + chunk) * p.G + g] = make_float2(mean, m2);
-  }
-}
-
-// One CTA: rows of one image, normalized with the merged statistics.
-template <int VEC>
-__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(const GnParams p, int chunks,
-                                                             int64_t rows_a) {
-  extern __shared__ float2 stat[];  // [G] (mean, 1 / sqrt(var + eps))
-  const int64_t b = blockIdx.x / unsigned(chunks);
-  const int cpg = p.C / p.G;
-  for (int g = threadIdx.x; g < p.G; g += kGnThreads) {
-    const float2* q = p.part + b * p.P * p.G + g;
-    auto rows_of = [&](int i) {
-      const int64_t left = p.S - int64_t(i) * p.rows_p;
-      return float(left < p.rows_p ? left : p.rows_p);
-    };
-    const float ref = q[0].x;
-    float mean = 0.0f;
-    for (int i = 1; i < p.P; ++i) mean = fmaf(rows_of(i), q[int64_t(i) * p.G].x - ref, mean);
-    mean = ref + mean / float(p.S);
-    float m2 = 0.0f;
-    for (int i = 0; i < p.P; ++i) {
-      const float2 v = q[int64_t(i) * p.G];
-      const float d = v.x - mean;
-      m2 += fmaf(rows_of(i) * float(cpg) * d, d, v.y);
-    }
-    const float var = m2 / (float(p.S) * float(cpg));
-    stat[g] = make_float2(mean, 1.0f / sqrtf(var + p.eps));
   }
   __syncthreads();
-  const int64_t r0 = int64_t(blockIdx.x % unsigned(chunks)) * rows_a;
-  const int64_t r1 = r0 + rows_a < p.S ? r0 + rows_a : p.S;
-  const int CV = p.C / VEC;
-  for (int v0 = 0; v0 < CV; v0 += kGnThreads) {
-    const int nv = CV - v0 < kGnThreads ? CV - v0 : kGnThreads;
-    const int RP = kGnThreads / nv;
-    const int rp = threadIdx.x / nv, cv = threadIdx.x % nv;
-    if (rp >= RP) continue;
-    const int c0 = (v0 + cv) * VEC;
-    float mean[VEC], a[VEC], be[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float2 s = stat[(c0 + i) / cpg];
-      mean[i] = s.x;
-      a[i] = s.y * (p.gamma ? __uint_as_float(uint32_t(p.gamma[c0 + i]) << 16) : 1.0f);
-      be[i] = p.beta ? __uint_as_float(uint32_t(p.beta[c0 + i]) << 16) : 0.0f;
+  for (int c = threadIdx.x; c < p.C; c += kGnThreads) {
+    const float2 st = stat[div_small(c, p.magic_cpg)];
+    if (c >= kGnThreads) {
+      ga = bf16_at(p.gamma, c, 1.0f);
+      be = bf16_at(p.beta, c, 0.0f);
     }
-    for (int64_t r = r0 + rp; r < r1; r += RP) {
-      const int64_t off = (b * p.S + r) * p.C + c0;
-      float v[VEC];
-      load_vec<VEC>(p.X + off, v);
-      constexpr int NP = (VEC + 1) / 2;
-      f2 z[NP];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float y = fmaf(v[i] - mean[i], a[i], be[i]);
-        if (i & 1) z[i / 2].y = y; else z[i / 2].x = y;
-      }
-      if constexpr (VEC == 1) z[0].y = 0.0f;
-      act_chunk<NP>(p.act, z);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = (i & 1) ? z[i / 2].y : z[i / 2].x;
-      store_vec<VEC>(p.Y + off, v);
-    }
+    coef[c] = st.x;
+    coef[p.C + c] = st.y * ga;
+    coef[2 * p.C + c] = be;
   }
+  __syncthreads();
+  with_act(p.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    Normalize<VEC> nz;
+    if (rp < RPa) {
+      nz.load(coef, p.C, cv * VEC);
+      uint16_t* y = p.Y + base + rp * p.C + cv * VEC;
+      int left = cnt;
+      while (left >= U) {
+        // this batch's rows are in `raw`; the next batch's go out first
+        V cur[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) cur[j] = raw[j];
+        x += U * step;
+        left -= U;
+        if (left >= U) {
+#pragma unroll
+          for (int j = 0; j < U; ++j) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+        } else {
+#pragma unroll
+          for (int j = 0; j < U - 1; ++j)
+            if (j < left) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) cur[j] = nz.template apply<ACT>(cur[j]);
+#pragma unroll
+        for (int j = 0; j < U; ++j) *reinterpret_cast<V*>(y + j * step) = cur[j];
+        y += U * step;
+      }
+#pragma unroll
+      for (int j = 0; j < U - 1; ++j)
+        if (j < left) *reinterpret_cast<V*>(y + j * step) = nz.template apply<ACT>(raw[j]);
+    }
+    // rows of more than kGnThreads vectors: the other columns
+    for (int c2 = nva + int(threadIdx.x); c2 < CV; c2 += kGnThreads) {
+      nz.load(coef, p.C, c2 * VEC);
+      for (int r = 0; r < rows; ++r) {
+        const int64_t off = base + int64_t(r) * p.C + c2 * VEC;
+        *reinterpret_cast<V*>(p.Y + off) =
+            nz.template apply<ACT>(*reinterpret_cast<const V*>(p.X + off));
+      }
+    }
+  });
 }
 
-// Row chunks per image: enough CTAs for two a multiprocessor, at most 64.
-int gn_chunks(int64_t B, int64_t S, int C, int sms) {
-  (void)C;
-  int64_t want = (2 * int64_t(sms) + B - 1) / B;
-  if (want > 64) want = 64;
-  if (want > S) want = S;
-  if (want < 1) want = 1;
-  const int64_t rows = (S + want - 1) / want;
-  return int((S + rows - 1) / rows);
+// ---------------------------------------------------------------------- plan
+namespace {
+
+int gcd(int a, int b) {
+  while (b) {
+    const int t = a % b;
+    a = b;
+    b = t;
+  }
+  return a;
 }
+
+unsigned magic_of(int d) { return d == 1 ? 0u : unsigned(((uint64_t(1) << 32) + d - 1) / d); }
+
+int log2_floor(int v) {
+  int l = 0;
+  while ((2 << l) <= v) ++l;
+  return l;
+}
+
+}  // namespace
+
+// Row chunks and vector width (see GnParams): one CTA an SM over the whole
+// batch, two where one leaves more than a tenth of the SMs idle; chunks of less
+// than 2^30 elements.
+void gn_plan(GnParams* p, int* vec, int sms) {
+  const int C = p->C, G = p->G, cpg = C / G;
+  p->cpg = cpg;
+  // the widest vectors whose slices of whole groups fit a CTA's threads
+  for (int v : {8, 4, 2, 1}) {
+    if (C % v != 0) continue;
+    const int unit = v / gcd(cpg, v);
+    if (unit > 1 && int64_t(unit) * cpg / v > kGnThreads) continue;
+    *vec = v;
+    p->gs = unit;
+    for (int gs = unit; gs <= G && int64_t(gs) * cpg / v <= kGnThreads; gs += unit)
+      if (G % gs == 0) p->gs = gs;
+    break;
+  }
+  int64_t want = sms / p->B;
+  if (want < 1 || double(want * p->B) < 0.9 * sms) want = 2 * int64_t(sms) / p->B;
+  const int64_t least = (p->S * C >> 30) + 1;
+  want = want > p->S ? p->S : want < least ? least : want;
+  const int64_t rows = (p->S + want - 1) / want;
+  p->rows_p = int(rows);
+  p->P = int((p->S + rows - 1) / rows);
+  p->rows_last = int(p->S - (p->P - 1) * rows);
+  p->n_full = float(rows) * float(cpg);
+  p->n_last = float(p->rows_last) * float(cpg);
+  p->inv_n = float(1.0 / (double(p->S) * cpg));
+  // statistics
+  p->inv_n_full = float(1.0 / (double(rows) * cpg));
+  p->inv_n_last = float(1.0 / (double(p->rows_last) * cpg));
+  p->nv = p->gs * cpg / *vec;
+  p->RP = p->nv <= kGnThreads ? kGnThreads / p->nv : 1;
+  p->magic_nv = magic_of(p->nv);
+  p->q_full = p->rows_p / p->RP;
+  p->q_last = p->rows_last / p->RP;
+  const int M = p->nv <= kGnThreads ? p->nv * *vec : kGnThreads * *vec;
+  const int gcpg = M / p->gs;
+  p->kk = M >= kGnThreads ? 1 : kGnThreads / M;
+  if (p->kk > p->RP) p->kk = p->RP;
+  p->magic_m = magic_of(M);
+  int lanes = 32;
+  while (lanes > 1 && (lanes * p->gs > kGnThreads || lanes >= 2 * gcpg)) lanes >>= 1;
+  p->lanes = lanes;
+  p->log_lanes = log2_floor(lanes);
+  // normalization
+  const int CV = C / *vec;
+  p->nva = CV < kGnThreads ? CV : kGnThreads;
+  p->RPa = kGnThreads / p->nva;
+  p->qa_full = p->rows_p / p->RPa;
+  p->qa_last = p->rows_last / p->RPa;
+  p->magic_nva = magic_of(p->nva);
+  p->magic_g = magic_of(G);
+  p->magic_cpg = magic_of(cpg);
+  p->ka = G >= kGnThreads ? 1 : kGnThreads / G;
+  if (p->ka > p->P) p->ka = p->P;
+  int la = 32;
+  while (la > 1 && (la * G > kGnThreads || la >= 2 * p->ka)) la >>= 1;
+  p->lanes_a = la;
+  p->log_lanes_a = log2_floor(la);
+}
+
+namespace {
+
+// The shared-memory limit of one kernel, set once on each device.
+struct AttrOnce {
+  std::atomic<unsigned long long> done{0};
+  cudaError_t set(const void* fn, size_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 template <int VEC>
-static cudaError_t launch_gn(const GnParams& p, int sms, cudaStream_t st) {
-  const size_t smem_s = sizeof(float2) * (size_t(p.C) + kGnThreads * VEC);
-  const size_t smem_a = sizeof(float2) * size_t(p.G);
-  cudaError_t e = cudaFuncSetAttribute(gn_stats_kernel<VEC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+cudaError_t launch_vec(const GnParams& p, cudaStream_t st) {
+  const int M = p.nv <= kGnThreads ? p.nv * VEC : kGnThreads * VEC;
+  const size_t smem_s =
+      sizeof(float2) * (size_t(kPartLd) * VEC + size_t(M > kGnThreads ? M : kGnThreads));
+  const size_t smem_a = sizeof(float2) * (size_t(p.G) + kGnThreads) + 4 * (3 * size_t(p.C) + 1);
+  static AttrOnce as, aa;
+  cudaError_t e = as.set((const void*)gn_stats_kernel<VEC>, 80 * 1024);
+  if (e == cudaSuccess) e = aa.set((const void*)gn_apply_kernel<VEC>, 176 * 1024);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(gn_apply_kernel<VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           96 * 1024);
-  if (e != cudaSuccess) return e;
-  gn_stats_kernel<VEC><<<unsigned(p.P * p.B), kGnThreads, smem_s, st>>>(p);
+  const unsigned zs = unsigned((p.B + 65534) / 65535);
+  const dim3 grid(unsigned(p.P), unsigned(p.B < 65535 ? p.B : 65535), zs);
+  gn_stats_kernel<VEC><<<grid, kGnThreads, smem_s, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  int64_t chunks = (8 * int64_t(sms) + p.B - 1) / p.B;
-  if (chunks > p.S) chunks = p.S;
-  const int64_t rows = (p.S + chunks - 1) / chunks;
-  chunks = (p.S + rows - 1) / rows;
-  gn_apply_kernel<VEC><<<unsigned(chunks * p.B), kGnThreads, smem_a, st>>>(p, int(chunks), rows);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kGnThreads);
+  cfg.dynamicSmemBytes = smem_a;
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gn_apply_kernel<VEC>, p);
 }
 
-cudaError_t launch_group_norm(const GnParams& p, int sms, cudaStream_t st) {
-  if (p.C % 8 == 0) return launch_gn<8>(p, sms, st);
-  if (p.C % 4 == 0) return launch_gn<4>(p, sms, st);
-  if (p.C % 2 == 0) return launch_gn<2>(p, sms, st);
-  return launch_gn<1>(p, sms, st);
+}  // namespace
+
+cudaError_t launch_group_norm(int vec, const GnParams& p, cudaStream_t st) {
+  switch (vec) {
+    case 8: return launch_vec<8>(p, st);
+    case 4: return launch_vec<4>(p, st);
+    case 2: return launch_vec<2>(p, st);
+    default: return launch_vec<1>(p, st);
+  }
 }
 
 }  // namespace hq

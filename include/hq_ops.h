@@ -34,8 +34,9 @@ extern "C" {
  *   HQ_ACT_SILU       z / (1 + e^-z)
  *   HQ_ACT_GELU       z Phi(z) = z (1 + erf(z / sqrt 2)) / 2
  *   HQ_ACT_GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
- * A NaN stays a NaN.  An infinite z gives what the formula gives in IEEE
- * arithmetic (silu and gelu of -infinity are NaN). */
+ * A NaN stays a NaN.  Silu and the gelus are taken to |error| <= 2^-20 (2^-16
+ * for HQ_ACT_GELU) of their value, plus 4e-18 (1.1e-7 for HQ_ACT_GELU); of
+ * -infinity they give their limit to that error. */
 enum {
   HQ_ACT_NONE = 0,
   HQ_ACT_RELU = 1,

@@ -8,7 +8,10 @@ Bounds.  u = 2^-24 is half a step of fp32 relative to a value.
   act        silu / gelu_tanh: exponential and reciprocal instructions of 2^-22
              each, the argument's rounding 3 u |u_arg|: relative error at most
              2^-20 (1 + |u_arg|), u_arg capped where the result vanishes;
-             gelu adds 1.4e-5 relative and 1.1e-7 absolute (its fit).
+             gelu adds 1.4e-5 relative and 1.1e-7 absolute (its fit).  All
+             three enter no lower than z = -44 (-7.6, -13.5), where z sigmoid(u)
+             is -44 / (1 + e^44) = -3.5e-18 (less for the others): below, the
+             result is off by at most 4e-18.
   slopes     |act'| <= 1.13 for all of them.
 The stored value is the rounding of an fp32 value within tol of the exact one;
 rounding is monotone, so it lies between the roundings of exact - tol and
@@ -46,8 +49,7 @@ def act_tol(z, act):
         arg = 1.6 * (z.abs() + 0.045 * z.abs() ** 3)
     if act == GELU:
         arg = z.abs() * (1.6 + 0.075 * z.abs() ** 2)
-    # results below the smallest normal fp32 may be flushed to zero
-    tol = 2.0 ** -20 * (1 + arg.clamp(max=128.0)) * a + 2.0 ** -126 * (1 + z.abs())
+    tol = 2.0 ** -20 * (1 + arg.clamp(max=128.0)) * a + 4e-18
     if act == GELU:
         tol = tol + 1.4e-5 * a + 1.1e-7
     return tol

@@ -134,6 +134,15 @@ def test_dense_nonfinite(hq):
                                want.nan_to_num(1.0, 2.0, 3.0))
             rest = [i for i in range(T) if i not in (1, 2)]
             assert bool(Y[rest].isfinite().all())
+        # a NaN weight: its own column only, under every activation
+        X, W = _bf(_randn(g, T, K)), _bf(_randn(g, N, K))
+        W[8, 5] = float("nan")
+        W[33, 5] = float("nan")
+        for act in sorted(ACTS.values()):
+            Y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+            hq.hq_dense(hq.DenseDesc(K, N), X, W, None, hq.Epilogue(act), Y)
+            cols = Y.isnan().any(dim=0).nonzero().flatten().tolist()
+            assert cols == [8, 33] and bool(Y[:, [8, 33]].isnan().all())
 
 
 @pytest.mark.parametrize("T", [1, 4, 40, 130, 1500])
@@ -385,16 +394,19 @@ def test_group_norm_offset_and_outliers(hq, B, S, C, G):
 
 
 def test_group_norm_nonfinite_stays_in_its_group(hq):
-    B, S, C, G = 2, 300, 64, 8
-    X = _bf(_randn(_gen(1), B, S, C))
-    X[0, 17, 3] = float("nan")
-    X[1, 200, 20] = float("inf")
-    Y = hq.GroupNorm(C, G, act=SILU)(X)
-    bad = Y.isnan().view(B, S, G, -1).any(dim=3).any(dim=1)
-    want = torch.zeros(B, G, dtype=torch.bool, device="cuda")
-    want[0, 0] = want[1, 2] = True
-    assert torch.equal(bad, want)
-    assert bool(Y.view(B, S, G, -1)[0, :, 0].isnan().all())
+    for C, G in ((64, 8), (72, 8), (63, 9), (40, 8)):  # groups of 8, 9, 7 and 5 channels
+        B, S = 2, 300
+        cpg = C // G
+        X = _bf(_randn(_gen(1), B, S, C))
+        X[0, 17, 3] = float("nan")
+        X[1, 200, 2 * cpg + 4] = float("inf")
+        for act in (SILU, GELU, GELU_TANH, RELU, NONE):
+            Y = hq.GroupNorm(C, G, act=act)(X)
+            bad = Y.isnan().view(B, S, G, -1).any(dim=3).any(dim=1)
+            want = torch.zeros(B, G, dtype=torch.bool, device="cuda")
+            want[0, 0] = want[1, 2] = True
+            assert torch.equal(bad, want)
+            assert bool(Y.view(B, S, G, -1)[0, :, 0].isnan().all())
 
 
 @pytest.mark.parametrize("B,S,C,G", [(2, 4096, 320, 32), (1, 1000, 77, 11), (1, 30000, 128, 32)])
