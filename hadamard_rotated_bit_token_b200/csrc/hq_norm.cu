@@ -244,9 +244,9 @@ __device__ __forceinline__ int64_t image_of_block() {
 }
 
 // One CTA: a chunk of rows of one image.  Thread rp * nv + cv walks rows rp,
-// rp + RP, ... of vector column cv with eight loads in flight.
+// rp + RP, ... of vector column cv with eight to sixteen loads in flight.
 template <int VEC>
-__global__ void __launch_bounds__(kGnThreads, 2) gn_stats_kernel(const GnParams p) {
+__global__ void __launch_bounds__(kGnThreads, 1) gn_stats_kernel(const GnParams p) {
   extern __shared__ float2 sm[];
   float2* part = sm;                   // [VEC][kPartLd]
   float2* sums = sm + VEC * kPartLd;   // [max(kGnThreads, channels of a pass)]
@@ -272,24 +272,35 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_stats_kernel(const GnParams 
         const int step = RP * p.C;
         const uint16_t* x = xs + rp * p.C + cv * VEC;
         const int cnt = rp < rem ? q + 1 : q;
+        // batches of U rows, the next batch's loads out before this one is added
+        constexpr int U = 8;
+        V raw[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          if (j < cnt) raw[j] = *reinterpret_cast<const V*>(x + j * step);
         ThreadStats<VEC> ts;
-        ts.start(*reinterpret_cast<const V*>(x));
-        int i = 0;
-        for (; i + 8 <= cnt; i += 8) {
-          V raw[8];
+        ts.start(raw[0]);
+        int left = cnt;
+        while (left >= U) {
+          V cur[U];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+          for (int j = 0; j < U; ++j) cur[j] = raw[j];
+          x += U * step;
+          left -= U;
+          if (left >= U) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ts.add(raw[j]);
-          x += 8 * step;
+            for (int j = 0; j < U; ++j) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+          } else {
+#pragma unroll
+            for (int j = 0; j < U - 1; ++j)
+              if (j < left) raw[j] = *reinterpret_cast<const V*>(x + j * step);
+          }
+#pragma unroll
+          for (int j = 0; j < U; ++j) ts.add(cur[j]);
         }
-        for (; i + 2 <= cnt; i += 2) {
-          const V r1 = *reinterpret_cast<const V*>(x), r2 = *reinterpret_cast<const V*>(x + step);
-          ts.add(r1);
-          ts.add(r2);
-          x += 2 * step;
-        }
-        if (i < cnt) ts.add(*reinterpret_cast<const V*>(x));
+#pragma unroll
+        for (int j = 0; j < U - 1; ++j)
+          if (j < left) ts.add(raw[j]);
         ts.finish(cnt, part);
       }
       __syncthreads();
