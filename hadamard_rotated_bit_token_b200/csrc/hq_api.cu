@@ -613,6 +613,21 @@ hq_status encode_out_bf16_raw(CUtensorMap* m, const void* base, int64_t rows, in
   return from_cu(r);
 }
 
+// [rows,N] bf16 in boxes of 32 rows x 64 columns (128 bytes), 128-byte swizzle.
+hq_status encode_box64_bf16(CUtensorMap* m, const void* base, int64_t rows, int N) {
+  return cached_tmap(TmapKey{5, base, rows, N, 0}, m, [&](CUtensorMap* o) {
+    cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(N) * 2u};
+    cuuint32_t box[2] = {64u, 32u};
+    cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = g_encode(o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return from_cu(r);
+  });
+}
+
 hq_status encode_kmajor_i8(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
   return cached_tmap(TmapKey{1, base, rows, K, box_rows}, m, [&](CUtensorMap* o) {
     return encode_kmajor_i8_raw(o, base, rows, K, box_rows);
@@ -760,6 +775,22 @@ hq_status check_epilogue(const hq_epilogue* ep, int64_t T, int N, const uint16_t
   return HQ_OK;
 }
 
+// The epilogue's part of p (a null ep: none), and the maps of Y and of the
+// residual (Y's again without one) for launch_gemm_ep.
+hq_status set_epilogue(GemmEpParams* p, const hq_epilogue* ep, const uint16_t* Y, int64_t T, int N,
+                       CUtensorMap* map_y, CUtensorMap* map_r) {
+  hq_status s = encode_box64_bf16(map_y, Y, T, N);
+  if (s != HQ_OK) return s;
+  *map_r = *map_y;
+  if (ep == nullptr) return HQ_OK;
+  p->act = ep->act;
+  p->residual = ep->residual;
+  p->gate = ep->gate;
+  p->gate_rows = ep->gate_rows;
+  return ep->residual != nullptr && ep->residual != Y ? encode_box64_bf16(map_r, ep->residual, T, N)
+                                                       : HQ_OK;
+}
+
 bool plain_epilogue(const hq_epilogue* ep) {
   return ep == nullptr ||
          (ep->act == HQ_ACT_NONE && ep->residual == nullptr && ep->gate == nullptr);
@@ -803,26 +834,16 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
   const GemmChoice gc =
       choose_gemm(T, N, K, dev->sm_count, clusters_max, variant, logo, packed);
   const int bn = gc.pair ? 256 : gc.bn;
-  CUtensorMap ta, tb, ty;
+  CUtensorMap maps[4];
+  CUtensorMap &ta = maps[0], &tb = maps[1], &ty = maps[2];
   s = packed ? encode_packed_a(&ta, a_codes, T, K) : encode_kmajor_i8(&ta, a_codes, T, K, 128);
   if (s != HQ_OK) return s;
   s = encode_kmajor_i8(&tb, w_codes, N, K, gc.pair ? 128 : bn);
   if (s != HQ_OK) return s;
-  s = encode_out_bf16(&ty, Y, T, N);
-  if (s != HQ_OK) return s;
   GemmEpParams p;  // the plain kernels take its GemmParams part
   std::memset(&p, 0, sizeof(p));
-  CUtensorMap tr;
-  const void* tmap_r = nullptr;
-  if (ep != nullptr) {
-    p.act = ep->act;
-    p.gate = ep->gate;
-    p.gate_rows = ep->gate_rows;
-    if (ep->residual != nullptr) {
-      if ((s = encode_out_bf16(&tr, ep->residual, T, N)) != HQ_OK) return s;
-      tmap_r = &tr;
-    }
-  }
+  s = ep != nullptr ? set_epilogue(&p, ep, Y, T, N, &ty, &maps[3]) : encode_out_bf16(&ty, Y, T, N);
+  if (s != HQ_OK) return s;
   p.a_scale = a_scale;
   p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
   {
@@ -855,7 +876,7 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
     const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
     const int clusters = int(tiles < clusters_max ? tiles : clusters_max);
     if (ep != nullptr)
-      return from_cuda(launch_gemm_pair_ep(false, &ta, &tb, &ty, tmap_r, p, clusters, st));
+      return from_cuda(launch_gemm_pair_ep(false, maps, p, clusters, st));
     return from_cuda(launch_gemm_pair(&ta, &tb, &ty, p, clusters, st));
   }
   p.num_m_tiles = int((T + 127) / 128);
@@ -863,7 +884,7 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
   const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
   const int grid = int(tiles < dev->sm_count ? tiles : dev->sm_count);
   if (ep != nullptr)
-    return from_cuda(launch_gemm_ep(false, bn, logo, packed, &ta, &tb, &ty, tmap_r, p, grid, st));
+    return from_cuda(launch_gemm_ep(false, bn, logo, packed, maps, p, grid, st));
   return from_cuda(launch_gemm(bn, logo, packed, &ta, &tb, &ty, p, grid, st));
 }
 
@@ -1640,22 +1661,12 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   const GemmChoice gc = choose_gemm(T, N, KB, dev->sm_count, pair_clusters(dev), HQ_GEMM_AUTO, 0,
                                     false);
   const int bn = gc.pair ? 256 : gc.bn;
-  CUtensorMap ta, tb, ty, tr;
-  if ((s = encode_kmajor_i8(&ta, X, T, KB, 128)) != HQ_OK) return s;
-  if ((s = encode_kmajor_i8(&tb, W, N, KB, gc.pair ? 128 : bn)) != HQ_OK) return s;
-  if ((s = encode_out_bf16(&ty, Y, T, N)) != HQ_OK) return s;
+  CUtensorMap maps[4];
+  if ((s = encode_kmajor_i8(&maps[0], X, T, KB, 128)) != HQ_OK) return s;
+  if ((s = encode_kmajor_i8(&maps[1], W, N, KB, gc.pair ? 128 : bn)) != HQ_OK) return s;
   GemmEpParams p;
   std::memset(&p, 0, sizeof(p));
-  const void* tmap_r = nullptr;
-  if (epilogue != nullptr) {
-    p.act = epilogue->act;
-    p.gate = epilogue->gate;
-    p.gate_rows = epilogue->gate_rows;
-    if (epilogue->residual != nullptr) {
-      if ((s = encode_out_bf16(&tr, epilogue->residual, T, N)) != HQ_OK) return s;
-      tmap_r = &tr;
-    }
-  }
+  if ((s = set_epilogue(&p, epilogue, Y, T, N, &maps[2], &maps[3])) != HQ_OK) return s;
   p.bias16 = bias;
   p.Y = Y;
   p.T = T;
@@ -1671,10 +1682,10 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   p.num_n_tiles = int(nt);
   if (gc.pair) {
     const int clusters = int(mt * nt < dev->pair_clusters ? mt * nt : dev->pair_clusters);
-    return from_cuda(launch_gemm_pair_ep(true, &ta, &tb, &ty, tmap_r, p, clusters, st));
+    return from_cuda(launch_gemm_pair_ep(true, maps, p, clusters, st));
   }
   const int grid = int(mt * nt < dev->sm_count ? mt * nt : dev->sm_count);
-  return from_cuda(launch_gemm_ep(true, bn, 0, false, &ta, &tb, &ty, tmap_r, p, grid, st));
+  return from_cuda(launch_gemm_ep(true, bn, 0, false, maps, p, grid, st));
 }
 
 }  // extern "C"

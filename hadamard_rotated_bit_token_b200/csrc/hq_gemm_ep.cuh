@@ -27,54 +27,44 @@ template <int KIND, int BN, int LOGO, bool PK>
 __global__ void __launch_bounds__(GemmCfg<KIND, BN, PK, true>::THREADS, 1)
     gemm_ep_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
-                   const int has_res, const GemmEpParams p) {
-  gemm_body<KIND, BN, LOGO, PK, true>(&tmA, &tmB, &tmY, has_res ? &tmR : nullptr, p);
+                   const GemmEpParams p) {
+  gemm_body<KIND, BN, LOGO, PK, true>(&tmA, &tmB, &tmY, p.residual ? &tmR : nullptr, p);
 }
 
 template <int KIND, int BN, int LOGO, bool PK>
-cudaError_t launch_ep_one(const void* tmap_a, const void* tmap_b, const void* tmap_y,
-                          const void* tmap_r, const GemmEpParams& p, int grid, cudaStream_t st) {
+cudaError_t launch_ep_one(const CUtensorMap* maps, const GemmEpParams& p, int grid,
+                          cudaStream_t st) {
   using C = GemmCfg<KIND, BN, PK, true>;
   static SmemAttr attr;
   cudaError_t e = attr.set((const void*)gemm_ep_kernel<KIND, BN, LOGO, PK>, C::SMEM);
   if (e != cudaSuccess) return e;
-  gemm_ep_kernel<KIND, BN, LOGO, PK><<<grid, C::THREADS, C::SMEM, st>>>(
-      *reinterpret_cast<const CUtensorMap*>(tmap_a), *reinterpret_cast<const CUtensorMap*>(tmap_b),
-      *reinterpret_cast<const CUtensorMap*>(tmap_y),
-      *reinterpret_cast<const CUtensorMap*>(tmap_r ? tmap_r : tmap_y), tmap_r ? 1 : 0, p);
+  gemm_ep_kernel<KIND, BN, LOGO, PK>
+      <<<grid, C::THREADS, C::SMEM, st>>>(maps[0], maps[1], maps[2], maps[3], p);
   return cudaGetLastError();
 }
 
 template <int KIND, int LOGO, bool PK>
-cudaError_t launch_ep_bn(int bn, const void* tmap_a, const void* tmap_b, const void* tmap_y,
-                         const void* tmap_r, const GemmEpParams& p, int grid, cudaStream_t st) {
+cudaError_t launch_ep_bn(int bn, const CUtensorMap* maps, const GemmEpParams& p, int grid,
+                         cudaStream_t st) {
   switch (bn) {
-    case 128:
-      return launch_ep_one<KIND, 128, LOGO, PK>(tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
+    case 64: return launch_ep_one<KIND, 64, LOGO, PK>(maps, p, grid, st);
+    case 128: return launch_ep_one<KIND, 128, LOGO, PK>(maps, p, grid, st);
+    case 192: return launch_ep_one<KIND, 192, LOGO, PK>(maps, p, grid, st);
     case 256:  // packed A's stages leave no tensor memory for 256-column tiles
-      if constexpr (!PK)
-        return launch_ep_one<KIND, 256, LOGO, PK>(tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
+      if constexpr (!PK) return launch_ep_one<KIND, 256, LOGO, PK>(maps, p, grid, st);
       return cudaErrorInvalidValue;
-    default:
-      if constexpr (LOGO <= 5) {
-        if (bn == 64)
-          return launch_ep_one<KIND, 64, LOGO, PK>(tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
-        if (bn == 192)
-          return launch_ep_one<KIND, 192, LOGO, PK>(tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
-      }
-      return cudaErrorInvalidValue;
+    default: return cudaErrorInvalidValue;
   }
 }
 
 template <bool PK>
-cudaError_t launch_ep_logo(int bn, int logo, const void* tmap_a, const void* tmap_b,
-                           const void* tmap_y, const void* tmap_r, const GemmEpParams& p, int grid,
-                           cudaStream_t st) {
+cudaError_t launch_ep_logo(int bn, int logo, const CUtensorMap* maps, const GemmEpParams& p,
+                           int grid, cudaStream_t st) {
   switch (logo) {
-    case 0: return launch_ep_bn<kI8, 0, PK>(bn, tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
-    case 4: return launch_ep_bn<kI8, 4, PK>(bn, tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
-    case 5: return launch_ep_bn<kI8, 5, PK>(bn, tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
-    case 6: return launch_ep_bn<kI8, 6, PK>(bn, tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
+    case 0: return launch_ep_bn<kI8, 0, PK>(bn, maps, p, grid, st);
+    case 4: return launch_ep_bn<kI8, 4, PK>(bn, maps, p, grid, st);
+    case 5: return launch_ep_bn<kI8, 5, PK>(bn, maps, p, grid, st);
+    case 6: return launch_ep_bn<kI8, 6, PK>(bn, maps, p, grid, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -4,10 +4,9 @@
 
 namespace hq {
 
-cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* tmap_a, const void* tmap_b,
-                                  const void* tmap_y, const void* tmap_r, const GemmEpParams& p,
+cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* maps, const GemmEpParams& p,
                                   int grid, cudaStream_t st) {
-  return launch_ep_logo<true>(bn, logo, tmap_a, tmap_b, tmap_y, tmap_r, p, grid, st);
+  return launch_ep_logo<true>(bn, logo, static_cast<const CUtensorMap*>(maps), p, grid, st);
 }
 
 }  // namespace hq

@@ -63,9 +63,9 @@
 // EP adds to the epilogue  Y = bf16(R + g * act(z))  (see epi_tile_ep): z is
 //   the value that the plain epilogue would round, act an elementwise
 //   activation in fp32, g a row of gate values shared by gate_rows rows of Y,
-//   R the residual.  R's 32 x 32 boxes travel by TMA into the staging boxes
-//   that the output leaves from, one box ahead of the arithmetic, so a box is
-//   read, added to and stored in place.
+//   R the residual.  The activation makes the epilogue as long as a short main
+//   loop, so these kernels run up to sixteen epilogue warps (64 columns each)
+//   instead of eight.
 // Two accumulators in tensor memory let the epilogue of one tile overlap the
 // main loop of the next.  Every wait is bounded; a timeout records
 // HQ_ERR_TIMEOUT in the device error word, and the CTA waits for every copy it
@@ -478,166 +478,145 @@ __device__ __forceinline__ void epi_tile(const GemmParams& p, const CUtensorMap*
 }
 
 // ------------------------------------- epilogue with activation and residual
-// One epilogue warp's stream of residual boxes.  The warp's chunks (32 rows x
-// 32 columns each) are numbered over all of its tiles; chunk j uses staging
-// box j % NBOX.  Lane 0 keeps NBOX - 1 loads of R in flight; the store of
-// chunk j - 1 has read its box before the load of chunk j + NBOX - 1 is
-// issued into it.
+// Each epilogue warp owns 32 rows x 64 columns of a tile and one staging box of
+// that shape (4 KB, 128-byte rows, 128-byte swizzle).  R's box arrives in it by
+// TMA, is added to in place, and leaves by TMA as Y's; the next tile's box of R
+// is fetched as soon as the store has read the box, and so travels during the
+// next main loop.  (Loads and stores from registers, 32 bytes a thread and row,
+// were tried: the 32 single-sector accesses of a warp instruction made the
+// epilogue of a 128 x 256 tile 11000 cycles instead of 4000.)
+constexpr int kEpBox = 32 * 128;
+
 struct ResStream {
   const CUtensorMap* tmR;  // null: no residual
-  uint64_t* bar;           // [NBOX] box loaded
-  uint8_t* stg;            // the warp's staging boxes
-  int tile, chunk;         // next chunk to load
-  uint32_t issued, used;   // chunks loaded and consumed so far (lane 0 counts issued)
+  uint64_t* bar;           // the box of R has arrived
+  uint8_t* box;
+  uint32_t issued, used;   // boxes asked for (lane 0) and consumed
 };
 
-// Lane 0: loads the next chunk's box, if there is one.  locate(tile, row0,
-// col0) gives the warp's first row and column in a tile.
-template <int NCH, int NBOX, class Locate>
-__device__ __forceinline__ void res_load_next(const GemmEpParams& p, ResStream& s, int num_tiles,
-                                              int step, Locate locate) {
-  if (s.tile >= num_tiles) return;
-  int row0, col0;
-  locate(s.tile, row0, col0);
-  col0 += s.chunk * 32;
-  const int box = int(s.issued % NBOX);
+// Lane 0: asks for R's box at (row0, col0), if it lies inside R.
+__device__ __forceinline__ void res_load(const GemmEpParams& p, ResStream& s, int row0, int col0) {
   if (row0 < p.T && col0 < p.N) {
-    mbar_arrive_expect_tx(&s.bar[box], kStageBox);
-    tma_load_2d(s.stg + box * kStageBox, s.tmR, col0, row0, &s.bar[box]);
+    mbar_arrive_expect_tx(s.bar, kEpBox);
+    tma_load_2d(s.box, s.tmR, col0, row0, s.bar);
   } else {
-    mbar_arrive(&s.bar[box]);  // nothing of R there: the box is not read
+    mbar_arrive(s.bar);  // nothing there: the box is not read
   }
   ++s.issued;
-  if (++s.chunk == NCH) {
-    s.chunk = 0;
-    s.tile += step;
-  }
 }
 
-// z (one chunk of this thread's row) -> act, gate, residual -> bf16 in the
-// chunk's staging box -> TMA store.  Returns false if a wait gave up.
-template <int NBOX, class LoadNext>
-__device__ __forceinline__ bool epi_store_ep(const GemmEpParams& p, const CUtensorMap* tmY,
-                                             ResStream& s, f2 (&z)[16], int col0, int row0,
-                                             const uint16_t* gate_row, int lane, const WaitCtl& wc,
-                                             LoadNext load_next) {
-  uint4 gv[4];
+// z (chunk c, 0 or 1, of this thread's row) -> R + g * act(z) -> bf16 in the
+// warp's box.
+__device__ __forceinline__ void epi_box_ep(const GemmEpParams& p, f2 (&z)[16], int c, int col,
+                                           const uint16_t* gate_row, bool has_res, uint8_t* box,
+                                           int lane) {
+  uint4 g[4];
   if (gate_row) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      gv[q] = col0 + 8 * q < p.N ? *reinterpret_cast<const uint4*>(gate_row + col0 + 8 * q)
-                                 : make_uint4(0, 0, 0, 0);
+      g[q] = col + 8 * q < p.N ? *reinterpret_cast<const uint4*>(gate_row + col + 8 * q)
+                               : make_uint4(0, 0, 0, 0);
   }
   act_chunk(p.act, z);
   if (gate_row) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t w[4] = {gv[q].x, gv[q].y, gv[q].z, gv[q].w};
+      const uint32_t w[4] = {g[q].x, g[q].y, g[q].z, g[q].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[4 * q + i] = mul2(z[4 * q + i], unpack_bf16x2(w[i]));
     }
   }
-  const int box = int(s.used % NBOX);
-  uint8_t* row = s.stg + box * kStageBox + lane * 64;
-  const int swz = (lane >> 1) & 3;  // 64-byte swizzle of this thread's row
-  const bool inside = col0 < p.N && row0 < p.T;
-  if (s.tmR) {
-    const bool got = mbar_wait(&s.bar[box], (s.used / NBOX) & 1u, wc);
-    if (!__all_sync(0xffffffffu, got)) return false;
-    if (inside) {
+  uint8_t* row = box + lane * 128;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 rv = *reinterpret_cast<const uint4*>(row + ((q ^ swz) << 4));
-        const uint32_t w[4] = {rv.x, rv.y, rv.z, rv.w};
+  for (int q = 0; q < 4; ++q) {
+    uint4* slot = reinterpret_cast<uint4*>(row + (((4 * c + q) ^ (lane & 7)) << 4));
+    if (has_res) {
+      const uint4 rv = *slot;
+      const uint32_t w[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[4 * q + i] = add2(z[4 * q + i], unpack_bf16x2(w[i]));
-      }
+      for (int i = 0; i < 4; ++i) z[4 * q + i] = add2(z[4 * q + i], unpack_bf16x2(w[i]));
     }
-  } else {
-    if (lane == 0) bulk_wait_group_read<NBOX - 1>();
-    __syncwarp();
+    *slot = make_uint4(pack_bf16x2(z[4 * q].x, z[4 * q].y),
+                       pack_bf16x2(z[4 * q + 1].x, z[4 * q + 1].y),
+                       pack_bf16x2(z[4 * q + 2].x, z[4 * q + 2].y),
+                       pack_bf16x2(z[4 * q + 3].x, z[4 * q + 3].y));
   }
-  uint32_t packed[16];
-  pack_chunk(z, packed);
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint4*>(row + ((q ^ swz) << 4)) =
-        make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    if (inside) tma_store_2d(tmY, s.stg + box * kStageBox, col0, row0);
-    bulk_commit_group();  // one group per chunk, empty past the edges
-    if (s.tmR) {
-      bulk_wait_group_read<1>();  // chunk j - 1's box has been read
-      load_next();
-    }
-  }
-  ++s.used;
-  return true;
 }
 
-// As epi_tile, ending in  Y = bf16(R + g * act(z)).
-template <int KIND, int HC, int W, int NBOX, int LOGO, int GMAX, class RelAcc, class RelPrm,
-          class LoadNext>
+// As epi_tile for the warp's 64 columns, ending in  Y = bf16(R + g * act(z)).
+// (next_row0, next_col0): the warp's corner in its next tile, next_row0 < 0 for
+// none.  Returns false if a wait gave up.
+template <int KIND, int W, int LOGO, class RelAcc, class RelPrm>
 __device__ __forceinline__ bool epi_tile_ep(const GemmEpParams& p, const CUtensorMap* tmY,
                                             ResStream& s, uint32_t t_addr, const EpiTile& e,
                                             const uint16_t* gate_row, const float* prm,
-                                            int prm_col, int lane, const WaitCtl& wc,
-                                            RelAcc release_acc, RelPrm release_params,
-                                            LoadNext load_next) {
-  constexpr int NCH = HC / 32;
-  constexpr int G = LOGO == 6 || (NCH % 2 == 0 && GMAX >= 2) ? 2 : 1;
-  static_assert(NCH % G == 0, "whole groups of chunks");
-  static_assert(LOGO == 0 || (LOGO >= 4 && LOGO <= 6),
-                "output blocks of 16 or 32 columns, or 64 over chunk pairs");
-#pragma unroll 1
-  for (int c0 = 0; c0 < NCH; c0 += G) {
-    uint32_t r[G][32];
+                                            int prm_col, int next_row0, int next_col0, int lane,
+                                            const WaitCtl& wc, RelAcc release_acc,
+                                            RelPrm release_params) {
+  static_assert(LOGO == 0 || (LOGO >= 4 && LOGO <= 6), "output blocks of 16, 32 or 64 columns");
+  const bool has_res = s.tmR != nullptr;
+  // the box: R's has arrived, or the previous tile's store has read it
+  if (has_res) {
+    const bool got = mbar_wait(s.bar, s.used & 1u, wc);
+    ++s.used;
+    if (!__all_sync(0xffffffffu, got)) return false;
+  } else {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+  if constexpr (LOGO < 6) {
 #pragma unroll
-    for (int c = 0; c < G; ++c) tmem_ld_32x32b_x32(t_addr + uint32_t((c0 + c) * 32), r[c]);
-    tmem_wait_ld();
-    if (c0 + G == NCH) release_acc();
-    if constexpr (LOGO < 6) {
-#pragma unroll
-      for (int c = 0; c < G; ++c) {
-        f2 z[16];
-        if constexpr (KIND == kBF16) {
-          epi_z_bf16(r[c], c0 + c, reinterpret_cast<const uint16_t*>(prm) + prm_col, z);
-        } else if constexpr (LOGO == 0) {
-          epi_z<W>(p, r[c], c0 + c, e, prm + prm_col, z);
-        } else {
-          epi_dequant<W>(p, r[c], c0 + c, e, prm + prm_col, z);
-          fwht_chunk<LOGO>(z);
-          epi_finish<W>(p, z, c0 + c, prm + prm_col);
-        }
-        if (c0 + c == NCH - 1) release_params();
-        if (!epi_store_ep<NBOX>(p, tmY, s, z, e.col_base + (c0 + c) * 32, e.row0, gate_row, lane,
-                                wc, load_next))
-          return false;
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(t_addr + uint32_t(c * 32), r);
+      tmem_wait_ld();
+      if (c == 1) release_acc();
+      f2 z[16];
+      if constexpr (KIND == kBF16) {
+        epi_z_bf16(r, c, reinterpret_cast<const uint16_t*>(prm) + prm_col, z);
+      } else if constexpr (LOGO == 0) {
+        epi_z<W>(p, r, c, e, prm + prm_col, z);
+      } else {
+        epi_dequant<W>(p, r, c, e, prm + prm_col, z);
+        fwht_chunk<LOGO>(z);
+        epi_finish<W>(p, z, c, prm + prm_col);
       }
-    } else {
-      f2 z[2][16];
+      if (c == 1) release_params();
+      epi_box_ep(p, z, c, e.col_base + c * 32, gate_row, has_res, s.box, lane);
+    }
+  } else {
+    f2 z[2][16];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        epi_dequant<W>(p, r[c], c0 + c, e, prm + prm_col, z[c]);
-        fwht_chunk<5>(z[c]);
-      }
-      // index bit 5: between the two 32-column chunks of each pair
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(t_addr + uint32_t(c * 32), r);
+      tmem_wait_ld();
+      if (c == 1) release_acc();
+      epi_dequant<W>(p, r, c, e, prm + prm_col, z[c]);
+      fwht_chunk<5>(z[c]);
+    }
+    // index bit 5: between the two 32-column chunks
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const f2 x = z[0][i], y = z[1][i];
-        z[0][i] = add2(x, y);
-        z[1][i] = sub2(x, y);
-      }
+    for (int i = 0; i < 16; ++i) {
+      const f2 x = z[0][i], y = z[1][i];
+      z[0][i] = add2(x, y);
+      z[1][i] = sub2(x, y);
+    }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) epi_finish<W>(p, z[c], c0 + c, prm + prm_col);
-      if (c0 + 2 == NCH) release_params();
+    for (int c = 0; c < 2; ++c) epi_finish<W>(p, z[c], c, prm + prm_col);
+    release_params();
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (!epi_store_ep<NBOX>(p, tmY, s, z[c], e.col_base + (c0 + c) * 32, e.row0, gate_row,
-                                lane, wc, load_next))
-          return false;
+    for (int c = 0; c < 2; ++c)
+      epi_box_ep(p, z[c], c, e.col_base + c * 32, gate_row, has_res, s.box, lane);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (e.row0 < p.T && e.col_base < p.N) tma_store_2d(tmY, s.box, e.col_base, e.row0);
+    bulk_commit_group();
+    if (has_res && next_row0 >= 0) {
+      bulk_wait_group_read<0>();
+      res_load(p, s, next_row0, next_col0);
     }
   }
   return true;
@@ -658,18 +637,19 @@ struct GemmCfg {
   static constexpr int P_BYTES = PK ? BM * BK / 2 : 0;  // packed A as loaded (64-byte swizzle)
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + P_BYTES;
   static constexpr uint32_t STAGE_TX = uint32_t(STAGE_BYTES);  // bytes the tensor loads bring
-  static constexpr int THREADS = kGemmThreads + (PK ? 32 * kConvWarps : 0);
+  static constexpr int EPW = EP ? BN / 16 : kEpiWarps;  // epilogue warps (EP: 64 columns each)
+  static constexpr int THREADS = 64 + 32 * EPW + (PK ? 32 * kConvWarps : 0);
   static constexpr int NBAR_STAGE = PK ? 3 : 2;  // full, empty (, converted)
-  static constexpr int HC = BN / 2;  // columns per epilogue warp
+  static constexpr int HC = BN * 4 / EPW;  // columns per epilogue warp
   // accumulator chunks read per tensor-memory wait: at most 3; one for packed
   // 192-column tiles, whose 448 threads leave 128 registers a thread
-  static constexpr int EPI_GMAX = EP ? (PK ? 1 : 2) : (PK && BN == 192) ? 1 : 3;
-  static constexpr int NBOX = EP ? 2 : 1;  // staging boxes per epilogue warp
-  static constexpr int EPI_STAGE_BYTES = NBOX * kStageBox;
+  static constexpr int EPI_GMAX = (PK && BN == 192) ? 1 : 3;
+  static constexpr int NBOX = 1;  // output staging boxes per epilogue warp
+  static constexpr int EPI_STAGE_BYTES = EP ? kEpBox : NBOX * kStageBox;
   static constexpr int RING_BYTES = 2 * 3 * BN * 4;
-  static constexpr int RES_BAR_BYTES = EP ? 8 * kEpiWarps * NBOX : 0;
+  static constexpr int RES_BAR_BYTES = EP ? 8 * EPW : 0;
   static constexpr int CTL_BYTES = 256 + RES_BAR_BYTES;
-  static constexpr int FIXED = kEpiWarps * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
+  static constexpr int FIXED = EPW * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
   static constexpr int STAGES_RAW = (kSmemLimit - FIXED) / STAGE_BYTES;
   // PK: A's stages (32 columns each) follow the two accumulators in the 512
   // columns of tensor memory; the barrier block holds 7 stages of 3 barriers
@@ -702,7 +682,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
   uint8_t* sB = smem + size_t(C::STAGES) * C::A_BYTES;
   uint8_t* sP = sB + size_t(C::STAGES) * C::B_BYTES;  // packed A (PK only)
   uint8_t* epi_stage = sP + size_t(C::STAGES) * C::P_BYTES;  // 1024-aligned
-  float* ring = reinterpret_cast<float*>(epi_stage + kEpiWarps * C::EPI_STAGE_BYTES);
+  float* ring = reinterpret_cast<float*>(epi_stage + C::EPW * C::EPI_STAGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring) + C::RING_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* conv = empty + C::STAGES;    // (PK) stage s's A widened into tensor memory
@@ -711,8 +691,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
   uint64_t* pfull = tempty + 2;          // [2] parameter slot loaded
   uint64_t* pempty = pfull + 2;          // [2] parameter slot read by the epilogue
   uint64_t* drain = pempty + 2;
-  uint64_t* rbar = drain + 1;            // [kEpiWarps][NBOX] residual box loaded (EP)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (EP ? kEpiWarps * C::NBOX : 0));
+  uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (EP)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (EP ? C::EPW : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -729,13 +709,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], kEpiWarps);  // one arrival per epilogue warp
+      mbar_init(&tempty[a], C::EPW);  // one arrival per epilogue warp
       mbar_init(&pfull[a], 1);
-      mbar_init(&pempty[a], kEpiWarps);
+      mbar_init(&pempty[a], C::EPW);
     }
     mbar_init(drain, 1);
     if constexpr (EP)
-      for (int i = 0; i < kEpiWarps * C::NBOX; ++i) mbar_init(&rbar[i], 1);
+      for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tmap(tmA);
@@ -862,26 +842,22 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
       mma_commit(drain);
       (void)mbar_wait(drain, 0, wc);
     }
-  } else if (warp < 2 + kEpiWarps) {
+  } else if (warp < 2 + C::EPW) {
     // ----------------------------------------------------------- epilogue
-    const int ew = warp - 2;         // 0 .. 7
+    const int ew = warp - 2;         // 0 .. EPW - 1
     const int quarter = warp & 3;    // TMEM lanes [32*quarter, 32*quarter + 32)
     const int half = ew >> 2;        // columns [half*HC, half*HC + HC) of the tile
     uint8_t* stg = epi_stage + ew * C::EPI_STAGE_BYTES;
+    [[maybe_unused]] ResStream rs{tmR, rbar + ew, stg, 0, 0};
     int acc_iter = 0;
     float sx_next = 0.0f, mt_next = 0.0f;
     if (KIND == kI8 && int(blockIdx.x) < num_tiles)
       load_row_params(p, int64_t(tile_m(p, int(blockIdx.x))) * BM + quarter * 32 + lane,
                       sx_next, mt_next);
-    [[maybe_unused]] ResStream rs{tmR, rbar + ew * C::NBOX, stg, int(blockIdx.x), 0, 0, 0};
-    auto locate = [&](int tile, int& row0, int& col0) {
-      row0 = tile_m(p, tile) * BM + quarter * 32;
-      col0 = tile_n(p, tile) * BN + half * C::HC;
-    };
     if constexpr (EP) {
-      if (tmR && lane == 0)
-        for (int i = 0; i < C::NBOX - 1; ++i)
-          res_load_next<C::HC / 32, C::NBOX>(p, rs, num_tiles, int(gridDim.x), locate);
+      if (tmR && lane == 0 && int(blockIdx.x) < num_tiles)
+        res_load(p, rs, tile_m(p, int(blockIdx.x)) * BM + quarter * 32,
+                 tile_n(p, int(blockIdx.x)) * BN + half * C::HC);
     }
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++acc_iter) {
       const int acc = acc_iter & 1;
@@ -921,11 +897,11 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
         if (lane == 0) mbar_arrive(&pempty[acc]);
       };
       if constexpr (EP) {
-        if (!epi_tile_ep<KIND, C::HC, BN, C::NBOX, LOGO, C::EPI_GMAX>(
-                p, tmY, rs, t_addr, e, gate_row_of(p, e.row), ring + acc * 3 * BN, half * C::HC,
-                lane, wc, release_acc, release_params, [&] {
-                  res_load_next<C::HC / 32, C::NBOX>(p, rs, num_tiles, int(gridDim.x), locate);
-                })) {
+        const int next_row0 = next < num_tiles ? tile_m(p, next) * BM + quarter * 32 : -1;
+        const int next_col0 = next < num_tiles ? tile_n(p, next) * BN + half * C::HC : 0;
+        if (!epi_tile_ep<KIND, BN, LOGO>(p, tmY, rs, t_addr, e, gate_row_of(p, e.row),
+                                         ring + acc * 3 * BN, half * C::HC, next_row0, next_col0,
+                                         lane, wc, release_acc, release_params)) {
           *abort_flag = 1;
           break;
         }
@@ -936,9 +912,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
       }
     }
     if constexpr (EP) {
-      if (tmR && lane == 0)  // after a give-up: the boxes still in flight land
-        for (; rs.used < rs.issued; ++rs.used)
-          (void)mbar_wait(&rs.bar[rs.used % C::NBOX], (rs.used / C::NBOX) & 1u, wc);
+      if (tmR && lane == 0 && rs.used < rs.issued)  // after a give-up: the box in flight lands
+        (void)mbar_wait(rs.bar, rs.used & 1u, wc);
     }
     if (lane == 0) bulk_wait_group<0>();  // all of this warp's stores are complete
     __syncwarp();
@@ -1009,13 +984,15 @@ struct PairCfg {
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // per CTA
-  static constexpr int HC = BN / 2;  // columns per epilogue warp
+  static constexpr int EPW = EP ? 16 : kEpiWarps;
+  static constexpr int THREADS = 64 + 32 * EPW;
+  static constexpr int HC = BN * 4 / EPW;    // columns per epilogue warp
   static constexpr int NBOX = 2;  // output staging boxes per epilogue warp
-  static constexpr int EPI_STAGE_BYTES = NBOX * kStageBox;
+  static constexpr int EPI_STAGE_BYTES = EP ? kEpBox : NBOX * kStageBox;
+  static constexpr int RES_BAR_BYTES = EP ? 8 * EPW : 0;
   static constexpr int RING_BYTES = 2 * 3 * BN * 4;
-  static constexpr int RES_BAR_BYTES = EP ? 8 * kEpiWarps * NBOX : 0;
   static constexpr int CTL_BYTES = 512;
-  static constexpr int FIXED = kEpiWarps * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
+  static constexpr int FIXED = EPW * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
   static constexpr int STAGES_RAW = (kSmemLimit - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   static constexpr int TMEM_COLS = tmem_cols_for(2 * BN);
@@ -1055,7 +1032,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   uint8_t* sA = smem;
   uint8_t* sB = smem + size_t(C::STAGES) * C::A_BYTES;
   uint8_t* epi_stage = sB + size_t(C::STAGES) * C::B_BYTES;  // 1024-aligned
-  float* ring = reinterpret_cast<float*>(epi_stage + kEpiWarps * C::EPI_STAGE_BYTES);
+  float* ring = reinterpret_cast<float*>(epi_stage + C::EPW * C::EPI_STAGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring) + C::RING_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
@@ -1063,8 +1040,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   uint64_t* pfull = tempty + 2;
   uint64_t* pempty = pfull + 2;
   uint64_t* drain = pempty + 2;
-  uint64_t* rbar = drain + 1;  // [kEpiWarps][NBOX] residual box loaded (EP)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (EP ? kEpiWarps * C::NBOX : 0));
+  uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (EP)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (EP ? C::EPW : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued_by = tmem_slot + 2;  // [2], rank 0: stages each CTA loaded
 
@@ -1073,7 +1050,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   const uint32_t rank = cluster_ctarank();
   const WaitCtl wc{p.err, p.wait_ns};
 
-  param_ring_zero<C::BN>(ring, threadIdx.x, kGemmThreads);
+  param_ring_zero<C::BN>(ring, threadIdx.x, C::THREADS);
   fence_proxy_async_smem();  // the zeros precede the ring's bulk copies
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -1082,13 +1059,13 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);
+      mbar_init(&tempty[a], 2 * C::EPW);
       mbar_init(&pfull[a], 1);
-      mbar_init(&pempty[a], kEpiWarps);
+      mbar_init(&pempty[a], C::EPW);
     }
     mbar_init(drain, 1);
     if constexpr (EP)
-      for (int i = 0; i < kEpiWarps * C::NBOX; ++i) mbar_init(&rbar[i], 1);
+      for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
     *abort_flag = 0;
     issued_by[0] = issued_by[1] = 0;
     fence_mbarrier_init();
@@ -1209,10 +1186,11 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    const int ew = warp - 2;         // 0 .. 7
+    const int ew = warp - 2;         // 0 .. EPW - 1
     const int quarter = warp & 3;    // TMEM lanes [32*quarter, 32*quarter + 32)
     const int half = ew >> 2;        // columns [half*HC, half*HC + HC) of the tile
     uint8_t* stg = epi_stage + ew * C::EPI_STAGE_BYTES;
+    [[maybe_unused]] ResStream rs{tmR, rbar + ew, stg, 0, 0};
     const uint32_t tempty0 = mapa_shared(tempty, 0);
     const int row_off = int(rank) * BM + quarter * 32 + lane;
     int acc_iter = 0;
@@ -1220,15 +1198,10 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     if (KIND == kI8 && cluster_id < num_tiles)
       load_row_params(p, int64_t(tile_m(p, cluster_id)) * C::BM_PAIR + row_off, sx_next,
                       mt_next);
-    [[maybe_unused]] ResStream rs{tmR, rbar + ew * C::NBOX, stg, cluster_id, 0, 0, 0};
-    auto locate = [&](int tile, int& row0, int& col0) {
-      row0 = tile_m(p, tile) * C::BM_PAIR + int(rank) * BM + quarter * 32;
-      col0 = tile_n(p, tile) * C::BN + half * C::HC;
-    };
     if constexpr (EP) {
-      if (tmR && lane == 0)
-        for (int i = 0; i < C::NBOX - 1; ++i)
-          res_load_next<C::HC / 32, C::NBOX>(p, rs, num_tiles, num_clusters, locate);
+      if (tmR && lane == 0 && cluster_id < num_tiles)
+        res_load(p, rs, tile_m(p, cluster_id) * C::BM_PAIR + int(rank) * BM + quarter * 32,
+                 tile_n(p, cluster_id) * C::BN + half * C::HC);
     }
     for (int tile = cluster_id; tile < num_tiles; tile += num_clusters, ++acc_iter) {
       const int acc = acc_iter & 1;
@@ -1268,11 +1241,12 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
         if (lane == 0) mbar_arrive(&pempty[acc]);
       };
       if constexpr (EP) {
-        if (!epi_tile_ep<KIND, C::HC, C::BN, C::NBOX, 0, 2>(
-                p, tmY, rs, t_addr, e, gate_row_of(p, e.row), ring + acc * 3 * C::BN,
-                half * C::HC, lane, wc, release_acc, release_params, [&] {
-                  res_load_next<C::HC / 32, C::NBOX>(p, rs, num_tiles, num_clusters, locate);
-                })) {
+        const int next_row0 =
+            next < num_tiles ? tile_m(p, next) * C::BM_PAIR + int(rank) * BM + quarter * 32 : -1;
+        const int next_col0 = next < num_tiles ? tile_n(p, next) * C::BN + half * C::HC : 0;
+        if (!epi_tile_ep<KIND, C::BN, 0>(p, tmY, rs, t_addr, e, gate_row_of(p, e.row),
+                                         ring + acc * 3 * C::BN, half * C::HC, next_row0,
+                                         next_col0, lane, wc, release_acc, release_params)) {
           *abort_flag = 1;
           break;
         }
@@ -1283,9 +1257,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
       }
     }
     if constexpr (EP) {
-      if (tmR && lane == 0)  // after a give-up: the boxes still in flight land
-        for (; rs.used < rs.issued; ++rs.used)
-          (void)mbar_wait(&rs.bar[rs.used % C::NBOX], (rs.used / C::NBOX) & 1u, wc);
+      if (tmR && lane == 0 && rs.used < rs.issued)  // after a give-up: the box in flight lands
+        (void)mbar_wait(rs.bar, rs.used & 1u, wc);
     }
     if (lane == 0) bulk_wait_group<0>();  // all of this warp's stores are complete
     __syncwarp();

@@ -126,24 +126,23 @@ int gemm_pair_stages();
 // The GEMM with an activation, a gate and a residual in its epilogue
 // (hq_gemm_ep.cu): Y = bf16(R + g * act(z)), z what the plain epilogue rounds.
 struct GemmEpParams : GemmParams {
-  int act;                // HQ_ACT_*
-  const uint16_t* gate;   // bf16 [ceil(T / gate_rows), N] or null
-  int64_t gate_rows;      // rows of Y per row of the gate
-  const uint16_t* bias16; // bf16 operands: bf16 bias [N] or null (p.bias is null)
+  int act;                   // HQ_ACT_*
+  const uint16_t* residual;  // bf16 [T,N] or null; may be Y
+  const uint16_t* gate;      // bf16 [ceil(T / gate_rows), N] or null
+  int64_t gate_rows;         // rows of Y per row of the gate
+  const uint16_t* bias16;    // bf16 operands: bf16 bias [N] or null (p.bias is null)
 };
 
-// As launch_gemm / launch_gemm_pair.  tmap_r: the residual's map, laid out as
-// tmap_y, or null.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as bytes
-// (p.K = bytes per row; logo 0, not packed).
-cudaError_t launch_gemm_ep(bool bf16, int bn, int logo, bool packed_a, const void* tmap_a,
-                           const void* tmap_b, const void* tmap_y, const void* tmap_r,
+// As launch_gemm / launch_gemm_pair.  maps: four CUtensorMap, A and B as there,
+// then Y and the residual (without one: any map) [T,N] bf16 with box {64, 32}
+// and 128-byte swizzle.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as
+// bytes (p.K = bytes per row; logo 0, not packed).  logo 6 takes any bn here.
+cudaError_t launch_gemm_ep(bool bf16, int bn, int logo, bool packed_a, const void* maps,
                            const GemmEpParams& p, int grid, cudaStream_t st);
-cudaError_t launch_gemm_pair_ep(bool bf16, const void* tmap_a, const void* tmap_b,
-                                const void* tmap_y, const void* tmap_r, const GemmEpParams& p,
-                                int clusters, cudaStream_t st);
+cudaError_t launch_gemm_pair_ep(bool bf16, const void* maps, const GemmEpParams& p, int clusters,
+                                cudaStream_t st);
 // The packed-code kernels of launch_gemm_ep (hq_gemm_ep_pk.cu).
-cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* tmap_a, const void* tmap_b,
-                                  const void* tmap_y, const void* tmap_r, const GemmEpParams& p,
+cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* maps, const GemmEpParams& p,
                                   int grid, cudaStream_t st);
 
 // MMA-only loop (the int8 tensor-core ceiling): `ctas` CTAs (an even number
