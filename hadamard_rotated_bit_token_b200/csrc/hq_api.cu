@@ -776,19 +776,21 @@ hq_status check_epilogue(const hq_epilogue* ep, int64_t T, int N, const uint16_t
 }
 
 // The epilogue's part of p (a null ep: none), and the maps of Y and of the
-// residual (Y's again without one) for launch_gemm_ep.
+// residual (Y's again without one) for launch_gemm_ep with tiles of bn columns.
 hq_status set_epilogue(GemmEpParams* p, const hq_epilogue* ep, const uint16_t* Y, int64_t T, int N,
-                       CUtensorMap* map_y, CUtensorMap* map_r) {
-  hq_status s = encode_box64_bf16(map_y, Y, T, N);
+                       int bn, CUtensorMap* map_y, CUtensorMap* map_r) {
+  if (ep != nullptr) {
+    p->act = ep->act;
+    p->residual = ep->residual;
+    p->gate = ep->gate;
+    p->gate_rows = ep->gate_rows;
+  }
+  hq_status s = bn == 256 ? encode_out_bf16(map_y, Y, T, N) : encode_box64_bf16(map_y, Y, T, N);
   if (s != HQ_OK) return s;
   *map_r = *map_y;
-  if (ep == nullptr) return HQ_OK;
-  p->act = ep->act;
-  p->residual = ep->residual;
-  p->gate = ep->gate;
-  p->gate_rows = ep->gate_rows;
-  return ep->residual != nullptr && ep->residual != Y ? encode_box64_bf16(map_r, ep->residual, T, N)
-                                                       : HQ_OK;
+  return bn != 256 && p->residual != nullptr && p->residual != Y
+             ? encode_box64_bf16(map_r, p->residual, T, N)
+             : HQ_OK;
 }
 
 bool plain_epilogue(const hq_epilogue* ep) {
@@ -842,7 +844,7 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
   if (s != HQ_OK) return s;
   GemmEpParams p;  // the plain kernels take its GemmParams part
   std::memset(&p, 0, sizeof(p));
-  s = ep != nullptr ? set_epilogue(&p, ep, Y, T, N, &ty, &maps[3]) : encode_out_bf16(&ty, Y, T, N);
+  s = ep != nullptr ? set_epilogue(&p, ep, Y, T, N, bn, &ty, &maps[3]) : encode_out_bf16(&ty, Y, T, N);
   if (s != HQ_OK) return s;
   p.a_scale = a_scale;
   p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
@@ -1666,7 +1668,7 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   if ((s = encode_kmajor_i8(&maps[1], W, N, KB, gc.pair ? 128 : bn)) != HQ_OK) return s;
   GemmEpParams p;
   std::memset(&p, 0, sizeof(p));
-  if ((s = set_epilogue(&p, epilogue, Y, T, N, &maps[2], &maps[3])) != HQ_OK) return s;
+  if ((s = set_epilogue(&p, epilogue, Y, T, N, bn, &maps[2], &maps[3])) != HQ_OK) return s;
   p.bias16 = bias;
   p.Y = Y;
   p.T = T;

@@ -15,7 +15,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
-  gemm_pair_body<kI8, false>(&tmA, &tmB, &tmY, nullptr, p);
+  gemm_pair_body<kI8, false>(&tmA, &tmB, &tmY, p);
 }
 
 // ------------------------------------------------- tensor-core ceiling

@@ -6,12 +6,11 @@
 namespace hq {
 
 template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KIND, true>::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_pair_ep_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmY,
-                        const __grid_constant__ CUtensorMap tmR, const GemmEpParams p) {
-  gemm_pair_body<KIND, true>(&tmA, &tmB, &tmY, p.residual ? &tmR : nullptr, p);
+                        const __grid_constant__ CUtensorMap tmY, const GemmEpParams p) {
+  gemm_pair_body<KIND, true>(&tmA, &tmB, &tmY, p);
 }
 
 template <int KIND>
@@ -22,7 +21,7 @@ static cudaError_t launch_pair_kind(const CUtensorMap* maps, const GemmEpParams&
   cudaError_t e = attr.set((const void*)gemm_pair_ep_kernel<KIND>, C::SMEM);
   if (e != cudaSuccess) return e;
   gemm_pair_ep_kernel<KIND>
-      <<<2 * clusters, C::THREADS, C::SMEM, st>>>(maps[0], maps[1], maps[2], maps[3], p);
+      <<<2 * clusters, kGemmThreads, C::SMEM, st>>>(maps[0], maps[1], maps[2], p);
   return cudaGetLastError();
 }
 

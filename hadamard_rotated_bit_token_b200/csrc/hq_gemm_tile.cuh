@@ -478,13 +478,24 @@ __device__ __forceinline__ void epi_tile(const GemmParams& p, const CUtensorMap*
 }
 
 // ------------------------------------- epilogue with activation and residual
-// Each epilogue warp owns 32 rows x 64 columns of a tile and one staging box of
-// that shape (4 KB, 128-byte rows, 128-byte swizzle).  R's box arrives in it by
-// TMA, is added to in place, and leaves by TMA as Y's; the next tile's box of R
-// is fetched as soon as the store has read the box, and so travels during the
-// next main loop.  (Loads and stores from registers, 32 bytes a thread and row,
-// were tried: the 32 single-sector accesses of a warp instruction made the
-// epilogue of a 128 x 256 tile 11000 cycles instead of 4000.)
+// Two layouts, by the tile (kWide): shared memory holds either more stages or
+// more epilogue.
+//   wide (tiles of up to 192 columns): a warp owns 32 rows x 64 columns and one
+//     staging box of that shape (4 KB, 128-byte rows, 128-byte swizzle).  R's
+//     box arrives in it by TMA, is added to in place, and leaves by TMA as Y's;
+//     the next tile's box of R is fetched as soon as the store has read the
+//     box, and so travels during the next main loop.  For short main loops,
+//     where the epilogue's arithmetic is the longer part.
+//   lean (256 columns and the CTA pair): eight warps of 128 columns with one
+//     32 x 32 box each, so that the operands keep four stages of 48 KB (six of
+//     32 KB in the pair); R comes from global memory into registers one chunk
+//     ahead.  For long main loops: 16384 x 4096 x 8192 in bf16 takes 764 us so,
+//     843 us with sixteen warps and four stages.
+// (Stores from registers, 32 bytes a thread and row, were tried: the 32
+// single-sector accesses of a warp instruction made the epilogue of a 128 x 256
+// tile 11000 cycles instead of 7000.)
+template <int BN>
+constexpr bool kWide = BN <= 192;
 constexpr int kEpBox = 32 * 128;
 
 struct ResStream {
@@ -622,6 +633,102 @@ __device__ __forceinline__ bool epi_tile_ep(const GemmEpParams& p, const CUtenso
   return true;
 }
 
+// Residual columns [col, col + 32) of `row` (zeros where there are none).
+__device__ __forceinline__ void load_residual(const GemmEpParams& p, int64_t row, int col,
+                                              uint4 (&v)[4]) {
+  if (p.residual == nullptr) return;
+  const uint16_t* src = p.residual + row * p.N + col;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    v[q] = row < p.T && col + 8 * q < p.N ? *reinterpret_cast<const uint4*>(src + 8 * q)
+                                          : make_uint4(0, 0, 0, 0);
+}
+
+// The lean layout: the warp's HC columns in 32-column chunks through one box.
+// `res` holds the first chunk's residual on entry and the next tile's (row
+// next_row, columns from next_col on; next_row < 0: none) on exit.
+template <int KIND, int HC, int W, int LOGO, class RelAcc, class RelPrm>
+__device__ __forceinline__ void epi_tile_lean(const GemmEpParams& p, const CUtensorMap* tmY,
+                                              uint32_t t_addr, const EpiTile& e,
+                                              const uint16_t* gate_row, const float* prm,
+                                              int prm_col, uint4 (&res)[4], int64_t next_row,
+                                              int next_col, uint8_t* box, int lane,
+                                              RelAcc release_acc, RelPrm release_params) {
+  constexpr int NCH = HC / 32;
+  auto finish = [&](f2 (&z)[16], int c) {
+    const int col = e.col_base + c * 32;
+    uint4 g[4];
+    if (gate_row) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        g[q] = col + 8 * q < p.N ? *reinterpret_cast<const uint4*>(gate_row + col + 8 * q)
+                                 : make_uint4(0, 0, 0, 0);
+    }
+    act_chunk(p.act, z);
+    if (gate_row) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t w[4] = {g[q].x, g[q].y, g[q].z, g[q].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[4 * q + i] = mul2(z[4 * q + i], unpack_bf16x2(w[i]));
+      }
+    }
+    if (p.residual != nullptr) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t w[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[4 * q + i] = add2(z[4 * q + i], unpack_bf16x2(w[i]));
+      }
+      if (c + 1 < NCH)
+        load_residual(p, e.row, col + 32, res);
+      else if (next_row >= 0)
+        load_residual(p, next_row, next_col, res);
+    }
+    uint32_t packed[16];
+    pack_chunk(z, packed);
+    if (lane == 0) bulk_wait_group_read<0>();  // the previous chunk's store has read the box
+    __syncwarp();
+    epi_store_chunk(p, tmY, packed, col, e.row0, box, lane);
+  };
+  constexpr int G = LOGO == 6 ? 2 : 1;
+#pragma unroll 1
+  for (int c0 = 0; c0 < NCH; c0 += G) {
+    f2 z[G][16];
+#pragma unroll
+    for (int c = 0; c < G; ++c) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(t_addr + uint32_t((c0 + c) * 32), r);
+      tmem_wait_ld();
+      if (c0 + c == NCH - 1) release_acc();
+      if constexpr (KIND == kBF16) {
+        epi_z_bf16(r, c0 + c, reinterpret_cast<const uint16_t*>(prm) + prm_col, z[c]);
+      } else if constexpr (LOGO == 0) {
+        epi_z<W>(p, r, c0 + c, e, prm + prm_col, z[c]);
+      } else {
+        epi_dequant<W>(p, r, c0 + c, e, prm + prm_col, z[c]);
+        fwht_chunk<(LOGO < 5 ? LOGO : 5)>(z[c]);
+      }
+    }
+    if constexpr (LOGO == 6) {
+      // index bit 5: between the two 32-column chunks
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const f2 x = z[0][i], y = z[1][i];
+        z[0][i] = add2(x, y);
+        z[1][i] = sub2(x, y);
+      }
+    }
+    if constexpr (LOGO > 0) {
+#pragma unroll
+      for (int c = 0; c < G; ++c) epi_finish<W>(p, z[c], c0 + c, prm + prm_col);
+    }
+    if (c0 + G == NCH) release_params();
+#pragma unroll
+    for (int c = 0; c < G; ++c) finish(z[c], c0 + c);
+  }
+}
+
 // This thread's row of the gate, or null (no gate, or a row past T).
 __device__ __forceinline__ const uint16_t* gate_row_of(const GemmEpParams& p, int64_t row) {
   return p.gate != nullptr && row < p.T ? p.gate + (row / p.gate_rows) * p.N : nullptr;
@@ -637,7 +744,8 @@ struct GemmCfg {
   static constexpr int P_BYTES = PK ? BM * BK / 2 : 0;  // packed A as loaded (64-byte swizzle)
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + P_BYTES;
   static constexpr uint32_t STAGE_TX = uint32_t(STAGE_BYTES);  // bytes the tensor loads bring
-  static constexpr int EPW = EP ? BN / 16 : kEpiWarps;  // epilogue warps (EP: 64 columns each)
+  static constexpr bool WIDE = EP && kWide<BN>;
+  static constexpr int EPW = WIDE ? BN / 16 : kEpiWarps;  // epilogue warps
   static constexpr int THREADS = 64 + 32 * EPW + (PK ? 32 * kConvWarps : 0);
   static constexpr int NBAR_STAGE = PK ? 3 : 2;  // full, empty (, converted)
   static constexpr int HC = BN * 4 / EPW;  // columns per epilogue warp
@@ -645,9 +753,9 @@ struct GemmCfg {
   // 192-column tiles, whose 448 threads leave 128 registers a thread
   static constexpr int EPI_GMAX = (PK && BN == 192) ? 1 : 3;
   static constexpr int NBOX = 1;  // output staging boxes per epilogue warp
-  static constexpr int EPI_STAGE_BYTES = EP ? kEpBox : NBOX * kStageBox;
+  static constexpr int EPI_STAGE_BYTES = WIDE ? kEpBox : NBOX * kStageBox;
   static constexpr int RING_BYTES = 2 * 3 * BN * 4;
-  static constexpr int RES_BAR_BYTES = EP ? 8 * EPW : 0;
+  static constexpr int RES_BAR_BYTES = WIDE ? 8 * EPW : 0;
   static constexpr int CTL_BYTES = 256 + RES_BAR_BYTES;
   static constexpr int FIXED = EPW * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
   static constexpr int STAGES_RAW = (kSmemLimit - FIXED) / STAGE_BYTES;
@@ -691,8 +799,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
   uint64_t* pfull = tempty + 2;          // [2] parameter slot loaded
   uint64_t* pempty = pfull + 2;          // [2] parameter slot read by the epilogue
   uint64_t* drain = pempty + 2;
-  uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (EP)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (EP ? C::EPW : 0));
+  uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (wide epilogue)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (C::WIDE ? C::EPW : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -714,7 +822,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
       mbar_init(&pempty[a], C::EPW);
     }
     mbar_init(drain, 1);
-    if constexpr (EP)
+    if constexpr (C::WIDE)
       for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -854,7 +962,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
     if (KIND == kI8 && int(blockIdx.x) < num_tiles)
       load_row_params(p, int64_t(tile_m(p, int(blockIdx.x))) * BM + quarter * 32 + lane,
                       sx_next, mt_next);
-    if constexpr (EP) {
+    [[maybe_unused]] uint4 res[4];
+    if constexpr (EP && !C::WIDE) {
+      if (int(blockIdx.x) < num_tiles)
+        load_residual(p, int64_t(tile_m(p, int(blockIdx.x))) * BM + quarter * 32 + lane,
+                      tile_n(p, int(blockIdx.x)) * BN + half * C::HC, res);
+    }
+    if constexpr (C::WIDE) {
       if (tmR && lane == 0 && int(blockIdx.x) < num_tiles)
         res_load(p, rs, tile_m(p, int(blockIdx.x)) * BM + quarter * 32,
                  tile_n(p, int(blockIdx.x)) * BN + half * C::HC);
@@ -899,11 +1013,18 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
       if constexpr (EP) {
         const int next_row0 = next < num_tiles ? tile_m(p, next) * BM + quarter * 32 : -1;
         const int next_col0 = next < num_tiles ? tile_n(p, next) * BN + half * C::HC : 0;
-        if (!epi_tile_ep<KIND, BN, LOGO>(p, tmY, rs, t_addr, e, gate_row_of(p, e.row),
-                                         ring + acc * 3 * BN, half * C::HC, next_row0, next_col0,
-                                         lane, wc, release_acc, release_params)) {
-          *abort_flag = 1;
-          break;
+        if constexpr (C::WIDE) {
+          if (!epi_tile_ep<KIND, BN, LOGO>(p, tmY, rs, t_addr, e, gate_row_of(p, e.row),
+                                           ring + acc * 3 * BN, half * C::HC, next_row0, next_col0,
+                                           lane, wc, release_acc, release_params)) {
+            *abort_flag = 1;
+            break;
+          }
+        } else {
+          epi_tile_lean<KIND, C::HC, BN, LOGO>(
+              p, tmY, t_addr, e, gate_row_of(p, e.row), ring + acc * 3 * BN, half * C::HC, res,
+              next_row0 < 0 ? -1 : int64_t(next_row0) + lane, next_col0, stg, lane, release_acc,
+              release_params);
         }
       } else {
         epi_tile<C::HC, BN, C::NBOX, LOGO, C::EPI_GMAX>(
@@ -911,7 +1032,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
             release_params);
       }
     }
-    if constexpr (EP) {
+    if constexpr (C::WIDE) {
       if (tmR && lane == 0 && rs.used < rs.issued)  // after a give-up: the box in flight lands
         (void)mbar_wait(rs.bar, rs.used & 1u, wc);
     }
@@ -984,15 +1105,12 @@ struct PairCfg {
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // per CTA
-  static constexpr int EPW = EP ? 16 : kEpiWarps;
-  static constexpr int THREADS = 64 + 32 * EPW;
-  static constexpr int HC = BN * 4 / EPW;    // columns per epilogue warp
-  static constexpr int NBOX = 2;  // output staging boxes per epilogue warp
-  static constexpr int EPI_STAGE_BYTES = EP ? kEpBox : NBOX * kStageBox;
-  static constexpr int RES_BAR_BYTES = EP ? 8 * EPW : 0;
+  static constexpr int HC = BN / 2;  // columns per epilogue warp
+  static constexpr int NBOX = EP ? 1 : 2;  // output staging boxes per epilogue warp
+  static constexpr int EPI_STAGE_BYTES = NBOX * kStageBox;
   static constexpr int RING_BYTES = 2 * 3 * BN * 4;
   static constexpr int CTL_BYTES = 512;
-  static constexpr int FIXED = EPW * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
+  static constexpr int FIXED = kEpiWarps * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
   static constexpr int STAGES_RAW = (kSmemLimit - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   static constexpr int TMEM_COLS = tmem_cols_for(2 * BN);
@@ -1001,7 +1119,7 @@ struct PairCfg {
   static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + FIXED;
   static_assert(B_BYTES % 1024 == 0, "stage bases must stay 1024-byte aligned");
   static_assert(STAGES >= 2, "shared memory budget");
-  static_assert(16 * STAGES + 96 + RES_BAR_BYTES <= CTL_BYTES, "barrier block");
+  static_assert(16 * STAGES + 96 <= CTL_BYTES, "barrier block");
   static_assert(SMEM <= size_t(kSmemLimit), "shared memory budget");
 };
 
@@ -1023,8 +1141,7 @@ struct PairCfg {
 // only one CTA loaded (after a bounded wait gave up).
 template <int KIND, bool EP>
 __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUtensorMap* tmB,
-                                               const CUtensorMap* tmY, const CUtensorMap* tmR,
-                                               const GemmArgs<EP>& p) {
+                                               const CUtensorMap* tmY, const GemmArgs<EP>& p) {
   using C = PairCfg<KIND, EP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -1032,7 +1149,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   uint8_t* sA = smem;
   uint8_t* sB = smem + size_t(C::STAGES) * C::A_BYTES;
   uint8_t* epi_stage = sB + size_t(C::STAGES) * C::B_BYTES;  // 1024-aligned
-  float* ring = reinterpret_cast<float*>(epi_stage + C::EPW * C::EPI_STAGE_BYTES);
+  float* ring = reinterpret_cast<float*>(epi_stage + kEpiWarps * C::EPI_STAGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring) + C::RING_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
@@ -1040,8 +1157,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   uint64_t* pfull = tempty + 2;
   uint64_t* pempty = pfull + 2;
   uint64_t* drain = pempty + 2;
-  uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (EP)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (EP ? C::EPW : 0));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued_by = tmem_slot + 2;  // [2], rank 0: stages each CTA loaded
 
@@ -1050,7 +1166,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   const uint32_t rank = cluster_ctarank();
   const WaitCtl wc{p.err, p.wait_ns};
 
-  param_ring_zero<C::BN>(ring, threadIdx.x, C::THREADS);
+  param_ring_zero<C::BN>(ring, threadIdx.x, kGemmThreads);
   fence_proxy_async_smem();  // the zeros precede the ring's bulk copies
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -1059,13 +1175,11 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * C::EPW);
+      mbar_init(&tempty[a], 2 * kEpiWarps);
       mbar_init(&pfull[a], 1);
-      mbar_init(&pempty[a], C::EPW);
+      mbar_init(&pempty[a], kEpiWarps);
     }
     mbar_init(drain, 1);
-    if constexpr (EP)
-      for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
     *abort_flag = 0;
     issued_by[0] = issued_by[1] = 0;
     fence_mbarrier_init();
@@ -1186,11 +1300,10 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    const int ew = warp - 2;         // 0 .. EPW - 1
+    const int ew = warp - 2;         // 0 .. 7
     const int quarter = warp & 3;    // TMEM lanes [32*quarter, 32*quarter + 32)
     const int half = ew >> 2;        // columns [half*HC, half*HC + HC) of the tile
     uint8_t* stg = epi_stage + ew * C::EPI_STAGE_BYTES;
-    [[maybe_unused]] ResStream rs{tmR, rbar + ew, stg, 0, 0};
     const uint32_t tempty0 = mapa_shared(tempty, 0);
     const int row_off = int(rank) * BM + quarter * 32 + lane;
     int acc_iter = 0;
@@ -1198,10 +1311,11 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     if (KIND == kI8 && cluster_id < num_tiles)
       load_row_params(p, int64_t(tile_m(p, cluster_id)) * C::BM_PAIR + row_off, sx_next,
                       mt_next);
+    [[maybe_unused]] uint4 res[4];
     if constexpr (EP) {
-      if (tmR && lane == 0 && cluster_id < num_tiles)
-        res_load(p, rs, tile_m(p, cluster_id) * C::BM_PAIR + int(rank) * BM + quarter * 32,
-                 tile_n(p, cluster_id) * C::BN + half * C::HC);
+      if (cluster_id < num_tiles)
+        load_residual(p, int64_t(tile_m(p, cluster_id)) * C::BM_PAIR + row_off,
+                      tile_n(p, cluster_id) * C::BN + half * C::HC, res);
     }
     for (int tile = cluster_id; tile < num_tiles; tile += num_clusters, ++acc_iter) {
       const int acc = acc_iter & 1;
@@ -1241,24 +1355,16 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
         if (lane == 0) mbar_arrive(&pempty[acc]);
       };
       if constexpr (EP) {
-        const int next_row0 =
-            next < num_tiles ? tile_m(p, next) * C::BM_PAIR + int(rank) * BM + quarter * 32 : -1;
-        const int next_col0 = next < num_tiles ? tile_n(p, next) * C::BN + half * C::HC : 0;
-        if (!epi_tile_ep<KIND, C::BN, 0>(p, tmY, rs, t_addr, e, gate_row_of(p, e.row),
-                                         ring + acc * 3 * C::BN, half * C::HC, next_row0,
-                                         next_col0, lane, wc, release_acc, release_params)) {
-          *abort_flag = 1;
-          break;
-        }
+        epi_tile_lean<KIND, C::HC, C::BN, 0>(
+            p, tmY, t_addr, e, gate_row_of(p, e.row), ring + acc * 3 * C::BN, half * C::HC, res,
+            next < num_tiles ? int64_t(tile_m(p, next)) * C::BM_PAIR + row_off : -1,
+            next < num_tiles ? tile_n(p, next) * C::BN + half * C::HC : 0, stg, lane, release_acc,
+            release_params);
       } else {
         epi_tile<C::HC, C::BN, C::NBOX, 0, 3>(p, tmY, t_addr, e,
                                               ring + acc * 3 * C::BN + half * C::HC, stg, lane,
                                               release_acc, release_params);
       }
-    }
-    if constexpr (EP) {
-      if (tmR && lane == 0 && rs.used < rs.issued)  // after a give-up: the box in flight lands
-        (void)mbar_wait(rs.bar, rs.used & 1u, wc);
     }
     if (lane == 0) bulk_wait_group<0>();  // all of this warp's stores are complete
     __syncwarp();

@@ -135,7 +135,8 @@ struct GemmEpParams : GemmParams {
 
 // As launch_gemm / launch_gemm_pair.  maps: four CUtensorMap, A and B as there,
 // then Y and the residual (without one: any map) [T,N] bf16 with box {64, 32}
-// and 128-byte swizzle.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as
+// and 128-byte swizzle; for bn 256 and the pair Y's box is {32, 32} with 64-byte
+// swizzle and the residual's map is not read.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as
 // bytes (p.K = bytes per row; logo 0, not packed).  logo 6 takes any bn here.
 cudaError_t launch_gemm_ep(bool bf16, int bn, int logo, bool packed_a, const void* maps,
                            const GemmEpParams& p, int grid, cudaStream_t st);
