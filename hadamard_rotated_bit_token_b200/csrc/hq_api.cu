@@ -793,6 +793,15 @@ hq_status set_epilogue(GemmEpParams* p, const hq_epilogue* ep, const uint16_t* Y
              : HQ_OK;
 }
 
+void set_rows_epilogue(RowsParams* p, const hq_epilogue* ep, uint16_t* Y) {
+  p->Y = Y;
+  if (ep == nullptr) return;
+  p->act = ep->act;
+  p->residual = ep->residual;
+  p->gate = ep->gate;
+  p->gate_rows = ep->gate_rows;
+}
+
 bool plain_epilogue(const hq_epilogue* ep) {
   return ep == nullptr ||
          (ep->act == HQ_ACT_NONE && ep->residual == nullptr && ep->gate == nullptr);
@@ -1635,6 +1644,33 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
   if (s == HQ_OK) s = check_epilogue(epilogue, T, desc->N, Y);
   if (s != HQ_OK || T == 0) return s;
   if (T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
+  // a few tokens: one pass over the weights (the weight-only form's transform
+  // and the raw accumulators need the tiles); without an epilogue the call is
+  // hq_linear whatever T is
+  if (T <= kRowsMaxT && desc->out_order <= 1 && acc_debug == nullptr && !plain_epilogue(epilogue)) {
+    DeviceState* dev;
+    s = device_state(&dev);
+    if (s != HQ_OK) return s;
+    const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
+    RowsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.A = reinterpret_cast<const uint8_t*>(a_codes);
+    p.B = reinterpret_cast<const uint8_t*>(w_codes);
+    p.row_bytes = desc->K;
+    p.a_row_bytes = code_row_bytes(desc);
+    p.T = int(T);
+    p.N = desc->N;
+    p.a_scale = a_scale;
+    p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
+    p.acc_unit = packed ? 0.0625f : 1.0f;
+    p.a_mean = a_mean;
+    p.w_scale = w_scale;
+    p.colsum = colsum;
+    p.bias = bias_f32;
+    set_rows_epilogue(&p, epilogue, Y);
+    return from_cuda(launch_rows(packed ? 2 : 1, p, dev->sm_count,
+                                 reinterpret_cast<cudaStream_t>(stream)));
+  }
   return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
                      plain_epilogue(epilogue) ? nullptr : epilogue, Y, acc_debug, stream);
 }
@@ -1660,6 +1696,19 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   if (s != HQ_OK) return s;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int KB = 2 * K;  // bytes per row of X and W
+  if (T <= kRowsMaxT) {  // a few tokens: one pass over W
+    RowsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.A = reinterpret_cast<const uint8_t*>(X);
+    p.B = reinterpret_cast<const uint8_t*>(W);
+    p.row_bytes = KB;
+    p.a_row_bytes = KB;
+    p.T = int(T);
+    p.N = N;
+    p.bias16 = bias;
+    set_rows_epilogue(&p, epilogue, Y);
+    return from_cuda(launch_rows(0, p, dev->sm_count, st));
+  }
   const GemmChoice gc = choose_gemm(T, N, KB, dev->sm_count, pair_clusters(dev), HQ_GEMM_AUTO, 0,
                                     false);
   const int bn = gc.pair ? 256 : gc.bn;

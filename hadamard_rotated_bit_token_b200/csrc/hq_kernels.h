@@ -146,6 +146,34 @@ cudaError_t launch_gemm_pair_ep(bool bf16, const void* maps, const GemmEpParams&
 cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* maps, const GemmEpParams& p,
                                   int grid, cudaStream_t st);
 
+// The products with an epilogue for at most kRowsMaxT tokens: hq_rows.cu.
+constexpr int kRowsMaxT = 8;
+struct RowsParams {
+  const uint8_t* A;          // [T, a_row_bytes]: bf16, int8 codes, or packed codes
+  const uint8_t* B;          // [N, row_bytes]: bf16 or int8 codes
+  int64_t row_bytes, a_row_bytes;
+  int T, N;
+  int log_wr;                // (launch_rows) row groups per CTA
+  // integer codes
+  const float* a_scale;      // [T] or [1]
+  int a_scale_per_row;
+  float acc_unit;            // 1, or 1/16 with packed codes
+  const float* a_mean;       // [T] or null
+  const float* w_scale;      // [N]
+  const float* colsum;       // [N] or null
+  const float* bias;         // [N] or null
+  // bf16
+  const uint16_t* bias16;    // [N] or null
+  // the epilogue
+  int act;
+  const uint16_t* residual;  // [T,N] or null; may be Y
+  const uint16_t* gate;      // [ceil(T / gate_rows), N] or null
+  int64_t gate_rows;
+  uint16_t* Y;               // [T,N]
+};
+// kind: 0 bf16, 1 int8 codes, 2 packed codes of A.
+cudaError_t launch_rows(int kind, RowsParams p, int sms, cudaStream_t st);
+
 // MMA-only loop (the int8 tensor-core ceiling): `ctas` CTAs (an even number
 // of them in clusters of two when pair), each issuing k_blocks x 4 MMAs of
 // 128 x 256 x 32 (pair: 256 x 256 x 32 per cluster, half per CTA).
