@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libhq.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["hq_api.cu", "hq_quant.cu", "hq_quant_act.cu", "hq_quant_act_spl2.cu",
            "hq_quant_act_spl3.cu", "hq_quant_act_spl4.cu", "hq_quant_act_big.cu", "hq_gemm.cu",
-           "hq_gemm_ep.cu", "hq_gemm_ep_pk.cu", "hq_norm.cu", "hq_rows.cu",
+           "hq_gemm_ep.cu", "hq_gemm_ep_pk.cu", "hq_norm.cu", "hq_rows.cu", "hq_splitk.cu",
            "hq_gw.cu"]
 HEADERS = ["hq_device.cuh", "hq_kernels.h", "hq_quant_common.cuh", "hq_act.cuh",
            "hq_gemm_tile.cuh", "hq_gemm_ep.cuh"]

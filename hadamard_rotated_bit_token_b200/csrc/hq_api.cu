@@ -793,13 +793,33 @@ hq_status set_epilogue(GemmEpParams* p, const hq_epilogue* ep, const uint16_t* Y
              : HQ_OK;
 }
 
-void set_rows_epilogue(RowsParams* p, const hq_epilogue* ep, uint16_t* Y) {
+template <class Params>
+void set_rows_epilogue(Params* p, const hq_epilogue* ep, uint16_t* Y) {
   p->Y = Y;
   if (ep == nullptr) return;
   p->act = ep->act;
   p->residual = ep->residual;
   p->gate = ep->gate;
   p->gate_rows = ep->gate_rows;
+}
+
+// Launches hq_splitk.cu's kernel on [T, row_bytes] by [N, row_bytes] operands;
+// the epilogue and scales of p are set.
+hq_status run_splitk(const DeviceState* dev, const SplitKPlan& pl, bool bf16, const void* A,
+                     int64_t T, const void* B, int N, int row_bytes, SplitKParams* p,
+                     cudaStream_t st) {
+  CUtensorMap tx, tw;
+  hq_status s = encode_kmajor_i8(&tx, A, T, row_bytes, pl.nt);
+  if (s != HQ_OK) return s;
+  if ((s = encode_kmajor_i8(&tw, B, N, row_bytes, 128)) != HQ_OK) return s;
+  p->T = T;
+  p->N = N;
+  p->split = pl.split;
+  p->k_blocks = pl.k_blocks;
+  p->num_n_tiles = (N + 127) / 128;
+  p->err = dev->err;
+  p->wait_ns = wait_ns();
+  return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, st));
 }
 
 bool plain_epilogue(const hq_epilogue* ep) {
@@ -1671,6 +1691,27 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
     return from_cuda(launch_rows(packed ? 2 : 1, p, dev->sm_count,
                                  reinterpret_cast<cudaStream_t>(stream)));
   }
+  // too few tiles for the GPU: K split over a cluster (codes one per byte)
+  if (desc->out_order <= 1 && acc_debug == nullptr && !plain_epilogue(epilogue) &&
+      desc->code_format == HQ_CODES_I8) {
+    DeviceState* dev;
+    s = device_state(&dev);
+    if (s != HQ_OK) return s;
+    const SplitKPlan pl = splitk_plan(T, desc->N, desc->K, dev->sm_count);
+    if (pl.split > 0) {
+      SplitKParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.a_scale = a_scale;
+      p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
+      p.a_mean = a_mean;
+      p.w_scale = w_scale;
+      p.colsum = colsum;
+      p.bias = bias_f32;
+      set_rows_epilogue(&p, epilogue, Y);
+      return run_splitk(dev, pl, false, a_codes, T, w_codes, desc->N, desc->K, &p,
+                        reinterpret_cast<cudaStream_t>(stream));
+    }
+  }
   return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
                      plain_epilogue(epilogue) ? nullptr : epilogue, Y, acc_debug, stream);
 }
@@ -1708,6 +1749,14 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
     p.bias16 = bias;
     set_rows_epilogue(&p, epilogue, Y);
     return from_cuda(launch_rows(0, p, dev->sm_count, st));
+  }
+  const SplitKPlan pl = splitk_plan(T, N, KB, dev->sm_count);
+  if (pl.split > 0) {  // too few tiles for the GPU
+    SplitKParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.bias16 = bias;
+    set_rows_epilogue(&p, epilogue, Y);
+    return run_splitk(dev, pl, true, X, T, W, N, KB, &p, st);
   }
   const GemmChoice gc = choose_gemm(T, N, KB, dev->sm_count, pair_clusters(dev), HQ_GEMM_AUTO, 0,
                                     false);

@@ -174,6 +174,39 @@ struct RowsParams {
 // kind: 0 bf16, 1 int8 codes, 2 packed codes of A.
 cudaError_t launch_rows(int kind, RowsParams p, int sms, cudaStream_t st);
 
+// The same with K split over a cluster: hq_splitk.cu.
+struct SplitKParams {
+  int64_t T;
+  int N;
+  int split, k_blocks, num_n_tiles;
+  // integer codes
+  const float* a_scale;      // [T] or [1]
+  int a_scale_per_row;
+  const float* a_mean;       // [T] or null
+  const float* w_scale;      // [N]
+  const float* colsum;       // [N] or null
+  const float* bias;         // [N] or null
+  // bf16
+  const uint16_t* bias16;    // [N] or null
+  // the epilogue
+  int act;
+  const uint16_t* residual;  // [T,N] or null; may be Y
+  const uint16_t* gate;      // [ceil(T / gate_rows), N] or null
+  int64_t gate_rows;
+  uint16_t* Y;               // [T,N]
+  unsigned int* err;
+  unsigned long long wait_ns;
+};
+// nt tokens (16, 32, 64 or 128) per tile; split 0: leave it to the tiles.
+struct SplitKPlan {
+  int nt, split, tiles, k_blocks;
+};
+SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms);
+// tmap_x: [T, row_bytes] as bytes with box {128, nt}; tmap_w: [N, row_bytes]
+// with box {128, 128}; 128-byte swizzle.
+cudaError_t launch_splitk(bool bf16, int nt, const void* tmap_x, const void* tmap_w,
+                          const SplitKParams& p, int tiles, cudaStream_t st);
+
 // MMA-only loop (the int8 tensor-core ceiling): `ctas` CTAs (an even number
 // of them in clusters of two when pair), each issuing k_blocks x 4 MMAs of
 // 128 x 256 x 32 (pair: 256 x 256 x 32 per cluster, half per CTA).
