@@ -63,14 +63,83 @@ struct SkCfg {
   static_assert(16 * STAGES + 32 <= 256, "barrier block");
 };
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
 
-__device__ __forceinline__ float2 bf16x2_at(const uint16_t* p) {
-  return unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p));
+// The split's partial sums of four weight rows from `src` on, added in rank
+// order, for two tokens at a time (all 2 SPLIT loads in flight at once).
+template <int KIND, int SPLIT>
+__device__ __forceinline__ void join(const float* src0, const float* src1, uint4 (&sum)[2]) {
+  uint4 v[2][SPLIT];
+#pragma unroll
+  for (int k = 0; k < SPLIT; ++k) {
+    v[0][k] = ld_cluster_v4(mapa_shared(src0, uint32_t(k)));
+    v[1][k] = ld_cluster_v4(mapa_shared(src1, uint32_t(k)));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sum[i] = v[i][0];
+#pragma unroll
+    for (int k = 1; k < SPLIT; ++k) {
+      const uint4 w = v[i][k];
+      if constexpr (KIND == kSkBF16) {
+        sum[i].x = __float_as_uint(__uint_as_float(sum[i].x) + __uint_as_float(w.x));
+        sum[i].y = __float_as_uint(__uint_as_float(sum[i].y) + __uint_as_float(w.y));
+        sum[i].z = __float_as_uint(__uint_as_float(sum[i].z) + __uint_as_float(w.z));
+        sum[i].w = __float_as_uint(__uint_as_float(sum[i].w) + __uint_as_float(w.w));
+      } else {
+        sum[i].x += w.x, sum[i].y += w.y, sum[i].z += w.z, sum[i].w += w.w;
+      }
+    }
+  }
+}
+
+// Four columns from n on of row t: sums -> the epilogue -> Y.
+template <int KIND>
+__device__ __forceinline__ void finish4(const SplitKParams& p, const uint4& s, int t, int n) {
+  f2 z[2];
+  if constexpr (KIND == kSkBF16) {
+    z[0] = pk(__uint_as_float(s.x), __uint_as_float(s.y));
+    z[1] = pk(__uint_as_float(s.z), __uint_as_float(s.w));
+    if (p.bias16) {
+      const uint2 b = *reinterpret_cast<const uint2*>(p.bias16 + n);
+      z[0] = add2(z[0], unpack_bf16x2(b.x));
+      z[1] = add2(z[1], unpack_bf16x2(b.y));
+    }
+  } else {
+    const float sx = p.a_scale_per_row ? p.a_scale[t] : p.a_scale[0];
+    const float4 sw = *reinterpret_cast<const float4*>(p.w_scale + n);
+    float4 c = p.bias ? *reinterpret_cast<const float4*>(p.bias + n) : make_float4(0, 0, 0, 0);
+    f2 c0 = pk(c.x, c.y), c1 = pk(c.z, c.w);
+    if (p.a_mean) {
+      const float m = p.a_mean[t];
+      const float4 cs = *reinterpret_cast<const float4*>(p.colsum + n);
+      c0 = fma2(pk(m, m), pk(cs.x, cs.y), c0);
+      c1 = fma2(pk(m, m), pk(cs.z, cs.w), c1);
+    }
+    z[0] = fma2(pk(__int2float_rn(int(s.x)), __int2float_rn(int(s.y))),
+                mul2(pk(sx, sx), pk(sw.x, sw.y)), c0);
+    z[1] = fma2(pk(__int2float_rn(int(s.z)), __int2float_rn(int(s.w))),
+                mul2(pk(sx, sx), pk(sw.z, sw.w)), c1);
+  }
+  act_chunk(p.act, z);
+  const int64_t off = int64_t(t) * p.N + n;
+  if (p.gate) {
+    const uint2 g = *reinterpret_cast<const uint2*>(p.gate + (t / p.gate_rows) * p.N + n);
+    z[0] = mul2(z[0], unpack_bf16x2(g.x));
+    z[1] = mul2(z[1], unpack_bf16x2(g.y));
+  }
+  if (p.residual) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + off);
+    z[0] = add2(z[0], unpack_bf16x2(r.x));
+    z[1] = add2(z[1], unpack_bf16x2(r.y));
+  }
+  *reinterpret_cast<uint2*>(p.Y + off) =
+      make_uint2(pack_bf16x2(z[0].x, z[0].y), pack_bf16x2(z[1].x, z[1].y));
 }
 
 }  // namespace
@@ -99,6 +168,11 @@ __global__ void __launch_bounds__(kSkThreads, 2)
   const int t0 = (tile / p.num_n_tiles) * NT;
   const int kb0 = int(int64_t(p.k_blocks) * rank / p.split);
   const int kb1 = int(int64_t(p.k_blocks) * (rank + 1) / p.split);
+  auto load = [&](int kb, int stage) {
+    mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+    tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, kb * 128, n0, &full[stage]);
+    tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, kb * 128, t0, &full[stage]);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -108,6 +182,9 @@ __global__ void __launch_bounds__(kSkThreads, 2)
     mbar_init(tfull, 1);
     *failed = 0;
     fence_mbarrier_init();
+    // the first round of stages is empty: its loads go out before the other
+    // warps and tensor memory are ready
+    for (int kb = kb0; kb < kb1 && kb < kb0 + C::STAGES; ++kb) load(kb, kb - kb0);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -120,16 +197,14 @@ __global__ void __launch_bounds__(kSkThreads, 2)
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      int stage = 0, issued = min(kb1 - kb0, C::STAGES);
+      uint32_t phase = 1;
+      for (int kb = kb0 + C::STAGES; kb < kb1; ++kb) {
         if (*failed || !mbar_wait(&empty[stage], phase ^ 1u, wc)) {
           *failed = 1;
           break;
         }
-        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
-        tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, kb * 128, n0, &full[stage]);
-        tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, kb * 128, t0, &full[stage]);
+        load(kb, stage);
         ++issued;
         if (++stage == C::STAGES) {
           stage = 0;
@@ -138,13 +213,8 @@ __global__ void __launch_bounds__(kSkThreads, 2)
       }
       if (*failed) {
         // the copies in flight land before the CTA can exit
-        for (int i = 0; i < C::STAGES && i < issued; ++i) {
-          if (--stage < 0) {
-            stage = C::STAGES - 1;
-            phase ^= 1u;
-          }
-          (void)mbar_wait(&full[stage], phase, wc);
-        }
+        for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+          (void)mbar_wait(&full[i % C::STAGES], uint32_t(i / C::STAGES) & 1u, wc);
       }
     }
   } else if (warp == 1) {
@@ -201,43 +271,27 @@ __global__ void __launch_bounds__(kSkThreads, 2)
   cluster_sync();  // every CTA's partial sums are in place
 
   if (!*failed) {
-    // pairs of weight rows of this CTA's share of the tokens
+    // this CTA's share of the tokens, a warp a token, four weight rows a lane
     const int tb = NT * rank / p.split, te = NT * (rank + 1) / p.split;
-    for (int i = int(threadIdx.x); i < (te - tb) * (kSkRows / 2); i += kSkThreads) {
-      const int tt = tb + i / (kSkRows / 2), j = 2 * (i % (kSkRows / 2));
-      const int t = t0 + tt, n = n0 + j;
-      if (t >= p.T || n >= p.N) continue;
-      const float* src = part + tt * kSkRows + j;
-      f2 z;
-      if constexpr (KIND == kSkBF16) {
-        f2 v = ld_cluster_f2(mapa_shared(src, 0));
-#pragma unroll 4
-        for (int k = 1; k < p.split; ++k) v = add2(v, ld_cluster_f2(mapa_shared(src, uint32_t(k))));
-        z = p.bias16 ? add2(v, bf16x2_at(p.bias16 + n)) : v;
-      } else {
-        int a = 0, b = 0;
-#pragma unroll 4
-        for (int k = 0; k < p.split; ++k) {
-          const f2 v = ld_cluster_f2(mapa_shared(src, uint32_t(k)));
-          a += __float_as_int(v.x);
-          b += __float_as_int(v.y);
-        }
-        const float sx = p.a_scale_per_row ? p.a_scale[t] : p.a_scale[0];
-        const float2 sw = *reinterpret_cast<const float2*>(p.w_scale + n);
-        f2 c = p.bias ? *reinterpret_cast<const float2*>(p.bias + n) : pk(0.0f, 0.0f);
-        if (p.a_mean) {
-          const float m = p.a_mean[t];
-          c = fma2(pk(m, m), *reinterpret_cast<const float2*>(p.colsum + n), c);
-        }
-        z = fma2(pk(__int2float_rn(a), __int2float_rn(b)), mul2(pk(sx, sx), sw), c);
+    const int n = n0 + 4 * lane;
+    constexpr int kWarps = kSkThreads / 32;
+    for (int tt = tb + warp; tt < te && t0 + tt < p.T; tt += 2 * kWarps) {
+      const int t2 = tt + kWarps < te ? tt + kWarps : tt;
+      const float* s0 = part + tt * kSkRows + 4 * lane;
+      const float* s1 = part + t2 * kSkRows + 4 * lane;
+      uint4 sum[2];
+      if (p.split == 8)
+        join<KIND, 8>(s0, s1, sum);
+      else if (p.split == 4)
+        join<KIND, 4>(s0, s1, sum);
+      else if (p.split == 2)
+        join<KIND, 2>(s0, s1, sum);
+      else
+        join<KIND, 1>(s0, s1, sum);
+      if (n < p.N) {
+        finish4<KIND>(p, sum[0], t0 + tt, n);
+        if (t2 != tt && t0 + t2 < p.T) finish4<KIND>(p, sum[1], t0 + t2, n);
       }
-      f2 zz[1] = {z};
-      act_chunk(p.act, zz);
-      z = zz[0];
-      const int64_t off = int64_t(t) * p.N + n;
-      if (p.gate) z = mul2(z, bf16x2_at(p.gate + (t / p.gate_rows) * p.N + n));
-      if (p.residual) z = add2(z, bf16x2_at(p.residual + off));
-      *reinterpret_cast<uint32_t*>(p.Y + off) = pack_bf16x2(z.x, z.y);
     }
   }
   cluster_sync();  // no CTA leaves while a peer may read its partial sums
