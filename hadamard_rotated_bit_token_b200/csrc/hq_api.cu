@@ -814,12 +814,12 @@ hq_status run_splitk(const DeviceState* dev, const SplitKPlan& pl, bool bf16, co
   if ((s = encode_kmajor_i8(&tw, B, N, row_bytes, 128)) != HQ_OK) return s;
   p->T = T;
   p->N = N;
-  p->split = pl.split;
+  p->log_split = pl.log_split;
   p->k_blocks = pl.k_blocks;
   p->num_n_tiles = (N + 127) / 128;
   p->err = dev->err;
   p->wait_ns = wait_ns();
-  return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, st));
+  return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, dev->sm_count, st));
 }
 
 bool plain_epilogue(const hq_epilogue* ep) {
@@ -1698,7 +1698,7 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
     s = device_state(&dev);
     if (s != HQ_OK) return s;
     const SplitKPlan pl = splitk_plan(T, desc->N, desc->K, dev->sm_count);
-    if (pl.split > 0) {
+    if (pl.use) {
       SplitKParams p;
       std::memset(&p, 0, sizeof(p));
       p.a_scale = a_scale;
@@ -1751,7 +1751,7 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
     return from_cuda(launch_rows(0, p, dev->sm_count, st));
   }
   const SplitKPlan pl = splitk_plan(T, N, KB, dev->sm_count);
-  if (pl.split > 0) {  // too few tiles for the GPU
+  if (pl.use) {  // too few tiles for the GPU
     SplitKParams p;
     std::memset(&p, 0, sizeof(p));
     p.bias16 = bias;

@@ -178,7 +178,8 @@ cudaError_t launch_rows(int kind, RowsParams p, int sms, cudaStream_t st);
 struct SplitKParams {
   int64_t T;
   int N;
-  int split, k_blocks, num_n_tiles;
+  int log_split, k_blocks, num_n_tiles;
+  int stages, log_nt;        // (launch_splitk)
   // integer codes
   const float* a_scale;      // [T] or [1]
   int a_scale_per_row;
@@ -197,15 +198,17 @@ struct SplitKParams {
   unsigned int* err;
   unsigned long long wait_ns;
 };
-// nt tokens (16, 32, 64 or 128) per tile; split 0: leave it to the tiles.
+// nt tokens (16, 32, 64 or 128) per tile, clusters of 2^log_split CTAs; !use:
+// leave it to the tiles.
 struct SplitKPlan {
-  int nt, split, tiles, k_blocks;
+  bool use;
+  int nt, log_split, tiles, k_blocks;
 };
 SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms);
 // tmap_x: [T, row_bytes] as bytes with box {128, nt}; tmap_w: [N, row_bytes]
 // with box {128, 128}; 128-byte swizzle.
 cudaError_t launch_splitk(bool bf16, int nt, const void* tmap_x, const void* tmap_w,
-                          const SplitKParams& p, int tiles, cudaStream_t st);
+                          const SplitKParams& p, int tiles, int sms, cudaStream_t st);
 
 // MMA-only loop (the int8 tensor-core ceiling): `ctas` CTAs (an even number
 // of them in clusters of two when pair), each issuing k_blocks x 4 MMAs of

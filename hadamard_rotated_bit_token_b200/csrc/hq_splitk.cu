@@ -8,11 +8,13 @@
 // the tokens its N side, so a batch of 16 tokens costs 16 columns of tensor
 // memory and of shared memory, not a tile of 128.  Warp 0 loads (TMA, 128-byte
 // swizzle, a ring of stages), warp 1 issues tcgen05.mma (kind::f16 or kind::i8)
-// into NT columns of tensor memory, warps 2..5 write the CTA's partial sums
-// [token][weight row] into shared memory over the spent stages.  After a cluster
-// barrier each CTA adds the split's partial sums, always in rank order, for its
-// share of the tokens through distributed shared memory, applies the epilogue
-// and stores.  Integer sums are exact; fp32 sums depend on the sizes alone.
+// into NT columns of tensor memory.  Every CTA owns NT / split tokens: warps
+// 2..5 read the CTA's partial sums from tensor memory and write each token's
+// into its owner's shared memory (distributed shared memory), and after one
+// cluster barrier the owner adds the split's partial sums in rank order, applies
+// the epilogue and stores.  Integer sums are exact; fp32 sums depend on the
+// sizes alone.  (Owners that fetched the partial sums instead paid the remote
+// latency after the barrier and a second barrier before they could leave.)
 //
 // Without the split a narrow layer is a few CTAs that walk all of K: 64 tokens,
 // K = 4608, N = 1152 in bf16 took 23.3 us by tiles of 128 x 192 on 6 SMs; by 9
@@ -31,7 +33,8 @@ namespace hq {
 namespace {
 
 constexpr int kSkRows = 128;     // weight rows per tile (MMA M)
-constexpr int kSkThreads = 192;  // producer, MMA issuer, four epilogue warps
+// producer, MMA issuer, four warps that read tensor memory; all eight join
+constexpr int kSkThreads = 256;
 constexpr int kSkI8 = 0, kSkBF16 = 1;
 
 // D format at bits 4-5 (s32 2, fp32 1), operand formats 1 (int8, bf16) at bits
@@ -53,92 +56,111 @@ struct SkCfg {
   static constexpr int W_BYTES = kSkRows * 128;
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-  // two CTAs an SM
-  static constexpr int STAGES = (110 * 1024) / STAGE_BYTES;
   static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
-  static constexpr int PART_BYTES = NT * kSkRows * 4;
-  static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + 256 + 1024;
-  static_assert(PART_BYTES <= STAGES * STAGE_BYTES, "partial sums fit the stages");
+  static constexpr int RECV_BYTES = NT * kSkRows * 4;  // [split][NT / split][kSkRows]
+  static constexpr int CTL_BYTES = 256;
+  // stages for two CTAs an SM (where that leaves three), and for one
+  static constexpr int STAGES_1 = (224 * 1024 - RECV_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES_2 =
+      (110 * 1024 - RECV_BYTES) / STAGE_BYTES >= 3 ? (110 * 1024 - RECV_BYTES) / STAGE_BYTES
+                                                   : STAGES_1;
+  static constexpr size_t smem(int stages) {
+    return size_t(stages) * STAGE_BYTES + RECV_BYTES + CTL_BYTES + 1024;
+  }
   static_assert(X_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
-  static_assert(16 * STAGES + 32 <= 256, "barrier block");
+  static_assert(16 * STAGES_1 + 32 <= CTL_BYTES, "barrier block");
 };
 
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The split's partial sums of four weight rows from `src` on, added in rank
-// order, for two tokens at a time (all 2 SPLIT loads in flight at once).
-template <int KIND, int SPLIT>
-__device__ __forceinline__ void join(const float* src0, const float* src1, uint4 (&sum)[2]) {
-  uint4 v[2][SPLIT];
-#pragma unroll
-  for (int k = 0; k < SPLIT; ++k) {
-    v[0][k] = ld_cluster_v4(mapa_shared(src0, uint32_t(k)));
-    v[1][k] = ld_cluster_v4(mapa_shared(src1, uint32_t(k)));
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// sum + the partial sums v, per element
+template <int KIND>
+__device__ __forceinline__ void add_parts(uint4& sum, const uint4& v) {
+  if constexpr (KIND == kSkBF16) {
+    sum.x = __float_as_uint(__uint_as_float(sum.x) + __uint_as_float(v.x));
+    sum.y = __float_as_uint(__uint_as_float(sum.y) + __uint_as_float(v.y));
+    sum.z = __float_as_uint(__uint_as_float(sum.z) + __uint_as_float(v.z));
+    sum.w = __float_as_uint(__uint_as_float(sum.w) + __uint_as_float(v.w));
+  } else {
+    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    sum[i] = v[i][0];
-#pragma unroll
-    for (int k = 1; k < SPLIT; ++k) {
-      const uint4 w = v[i][k];
-      if constexpr (KIND == kSkBF16) {
-        sum[i].x = __float_as_uint(__uint_as_float(sum[i].x) + __uint_as_float(w.x));
-        sum[i].y = __float_as_uint(__uint_as_float(sum[i].y) + __uint_as_float(w.y));
-        sum[i].z = __float_as_uint(__uint_as_float(sum[i].z) + __uint_as_float(w.z));
-        sum[i].w = __float_as_uint(__uint_as_float(sum[i].w) + __uint_as_float(w.w));
-      } else {
-        sum[i].x += w.x, sum[i].y += w.y, sum[i].z += w.z, sum[i].w += w.w;
-      }
+}
+
+// What the epilogue needs of four columns (the same for every token), and of a
+// token's four outputs; loaded before the sums they are added to are there.
+struct SkCols {
+  float4 sw, b, cs;
+};
+struct SkRow {
+  float sx, m;
+  uint2 gate, res;
+};
+
+template <int KIND>
+__device__ __forceinline__ void load_cols(const SplitKParams& p, int n, SkCols& c) {
+  c.b = c.cs = c.sw = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (n >= p.N) return;
+  if constexpr (KIND == kSkBF16) {
+    if (p.bias16) {
+      const uint2 b = *reinterpret_cast<const uint2*>(p.bias16 + n);
+      const f2 lo = unpack_bf16x2(b.x), hi = unpack_bf16x2(b.y);
+      c.b = make_float4(lo.x, lo.y, hi.x, hi.y);
     }
+  } else {
+    c.sw = *reinterpret_cast<const float4*>(p.w_scale + n);
+    if (p.bias) c.b = *reinterpret_cast<const float4*>(p.bias + n);
+    if (p.a_mean) c.cs = *reinterpret_cast<const float4*>(p.colsum + n);
   }
+}
+
+template <int KIND>
+__device__ __forceinline__ void load_row(const SplitKParams& p, int64_t t, int n, SkRow& r) {
+  r.sx = r.m = 0.0f;
+  r.gate = r.res = make_uint2(0, 0);
+  if (t >= p.T || n >= p.N) return;
+  if constexpr (KIND == kSkI8) {
+    r.sx = p.a_scale_per_row ? p.a_scale[t] : p.a_scale[0];
+    if (p.a_mean) r.m = p.a_mean[t];
+  }
+  if (p.gate) r.gate = *reinterpret_cast<const uint2*>(p.gate + (t / p.gate_rows) * p.N + n);
+  if (p.residual) r.res = *reinterpret_cast<const uint2*>(p.residual + t * p.N + n);
 }
 
 // Four columns from n on of row t: sums -> the epilogue -> Y.
 template <int KIND>
-__device__ __forceinline__ void finish4(const SplitKParams& p, const uint4& s, int t, int n) {
+__device__ __forceinline__ void finish4(const SplitKParams& p, const uint4& s, const SkCols& c,
+                                        const SkRow& r, int64_t t, int n) {
   f2 z[2];
   if constexpr (KIND == kSkBF16) {
-    z[0] = pk(__uint_as_float(s.x), __uint_as_float(s.y));
-    z[1] = pk(__uint_as_float(s.z), __uint_as_float(s.w));
-    if (p.bias16) {
-      const uint2 b = *reinterpret_cast<const uint2*>(p.bias16 + n);
-      z[0] = add2(z[0], unpack_bf16x2(b.x));
-      z[1] = add2(z[1], unpack_bf16x2(b.y));
-    }
+    z[0] = add2(pk(__uint_as_float(s.x), __uint_as_float(s.y)), pk(c.b.x, c.b.y));
+    z[1] = add2(pk(__uint_as_float(s.z), __uint_as_float(s.w)), pk(c.b.z, c.b.w));
   } else {
-    const float sx = p.a_scale_per_row ? p.a_scale[t] : p.a_scale[0];
-    const float4 sw = *reinterpret_cast<const float4*>(p.w_scale + n);
-    float4 c = p.bias ? *reinterpret_cast<const float4*>(p.bias + n) : make_float4(0, 0, 0, 0);
-    f2 c0 = pk(c.x, c.y), c1 = pk(c.z, c.w);
-    if (p.a_mean) {
-      const float m = p.a_mean[t];
-      const float4 cs = *reinterpret_cast<const float4*>(p.colsum + n);
-      c0 = fma2(pk(m, m), pk(cs.x, cs.y), c0);
-      c1 = fma2(pk(m, m), pk(cs.z, cs.w), c1);
-    }
+    const f2 sx = pk(r.sx, r.sx), m = pk(r.m, r.m);
     z[0] = fma2(pk(__int2float_rn(int(s.x)), __int2float_rn(int(s.y))),
-                mul2(pk(sx, sx), pk(sw.x, sw.y)), c0);
+                mul2(sx, pk(c.sw.x, c.sw.y)), fma2(m, pk(c.cs.x, c.cs.y), pk(c.b.x, c.b.y)));
     z[1] = fma2(pk(__int2float_rn(int(s.z)), __int2float_rn(int(s.w))),
-                mul2(pk(sx, sx), pk(sw.z, sw.w)), c1);
+                mul2(sx, pk(c.sw.z, c.sw.w)), fma2(m, pk(c.cs.z, c.cs.w), pk(c.b.z, c.b.w)));
   }
   act_chunk(p.act, z);
-  const int64_t off = int64_t(t) * p.N + n;
   if (p.gate) {
-    const uint2 g = *reinterpret_cast<const uint2*>(p.gate + (t / p.gate_rows) * p.N + n);
-    z[0] = mul2(z[0], unpack_bf16x2(g.x));
-    z[1] = mul2(z[1], unpack_bf16x2(g.y));
+    z[0] = mul2(z[0], unpack_bf16x2(r.gate.x));
+    z[1] = mul2(z[1], unpack_bf16x2(r.gate.y));
   }
   if (p.residual) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + off);
-    z[0] = add2(z[0], unpack_bf16x2(r.x));
-    z[1] = add2(z[1], unpack_bf16x2(r.y));
+    z[0] = add2(z[0], unpack_bf16x2(r.res.x));
+    z[1] = add2(z[1], unpack_bf16x2(r.res.y));
   }
-  *reinterpret_cast<uint2*>(p.Y + off) =
+  *reinterpret_cast<uint2*>(p.Y + t * p.N + n) =
       make_uint2(pack_bf16x2(z[0].x, z[0].y), pack_bf16x2(z[1].x, z[1].y));
 }
 
@@ -151,160 +173,184 @@ __global__ void __launch_bounds__(kSkThreads, 2)
   using C = SkCfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int stages = p.stages;
   uint8_t* sW = smem;
-  uint8_t* sX = smem + size_t(C::STAGES) * C::W_BYTES;
-  float* part = reinterpret_cast<float*>(smem);  // [NT][kSkRows], over the stages
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
+  uint8_t* sX = smem + size_t(stages) * C::W_BYTES;
+  uint32_t* recv = reinterpret_cast<uint32_t*>(smem + size_t(stages) * C::STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(recv + C::RECV_BYTES / 4);
+  uint64_t* empty = full + stages;
+  uint64_t* tfull = empty + stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{p.err, p.wait_ns};
   const int rank = int(cluster_ctarank());
-  const int tile = int(blockIdx.x) / p.split;
-  const int n0 = (tile % p.num_n_tiles) * kSkRows;
-  const int t0 = (tile / p.num_n_tiles) * NT;
-  const int kb0 = int(int64_t(p.k_blocks) * rank / p.split);
-  const int kb1 = int(int64_t(p.k_blocks) * (rank + 1) / p.split);
-  auto load = [&](int kb, int stage) {
-    mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
-    tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, kb * 128, n0, &full[stage]);
-    tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, kb * 128, t0, &full[stage]);
-  };
+  const int log_own = p.log_nt - p.log_split;  // tokens per owner
+  const int tile = int(blockIdx.x) >> p.log_split;
+  const int tile_t = tile / p.num_n_tiles;
+  const int n0 = (tile - tile_t * p.num_n_tiles) * kSkRows;
+  const int t0 = tile_t * NT;
+  const int kb0 = (p.k_blocks * rank) >> p.log_split;
+  const int nkb = ((p.k_blocks * (rank + 1)) >> p.log_split) - kb0;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    mbar_init(tfull, 1);
-    *failed = 0;
-    fence_mbarrier_init();
-    // the first round of stages is empty: its loads go out before the other
-    // warps and tensor memory are ready
-    for (int kb = kb0; kb < kb1 && kb < kb0 + C::STAGES; ++kb) load(kb, kb - kb0);
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
+  // every CTA of the cluster has started before any writes to another
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0, issued = min(kb1 - kb0, C::STAGES);
-      uint32_t phase = 1;
-      for (int kb = kb0 + C::STAGES; kb < kb1; ++kb) {
-        if (*failed || !mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+      for (int s = 0; s < 2 * stages + 1; ++s) mbar_init(&full[s], 1);  // full, empty, tfull
+      *failed = 0;
+      fence_mbarrier_init();
+    }
+    __syncwarp();
+    // the others wait for the barriers and tensor memory; this warp goes on
+    asm volatile("bar.arrive 1, %0;" ::"n"(kSkThreads) : "memory");
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int i = 0;
+      for (; i < nkb; ++i) {
+        if (i >= stages && !mbar_wait(&empty[stage], phase ^ 1u, wc)) {
           *failed = 1;
           break;
         }
-        load(kb, stage);
-        ++issued;
-        if (++stage == C::STAGES) {
+        const int x = (kb0 + i) * 128;
+        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+        tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, x, n0, &full[stage]);
+        tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, x, t0, &full[stage]);
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (*failed) {
-        // the copies in flight land before the CTA can exit
-        for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
-          (void)mbar_wait(&full[i % C::STAGES], uint32_t(i / C::STAGES) & 1u, wc);
-      }
+      // after a give-up the copies in flight land before the CTA can exit
+      if (i < nkb)
+        for (int j = i > stages ? i - stages : 0; j < i; ++j)
+          (void)mbar_wait(&full[j % stages], uint32_t(j / stages) & 1u, wc);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      const uint32_t w_base = smem_u32(sW), x_base = smem_u32(sX);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (*failed || !mbar_wait(&full[stage], phase, wc)) {
-          *failed = 1;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t wd = sk_desc(w_base + uint32_t(stage) * C::W_BYTES);
-        const uint64_t xd = sk_desc(x_base + uint32_t(stage) * C::X_BYTES);
+  } else {
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+      tc_fence_before();
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kSkThreads) : "memory");
+    tc_fence_after();
+  }
+
+  // what the epilogue needs from global memory, in flight during the product:
+  // a warp a token (two at a time), four weight rows a lane
+  const int n = n0 + 4 * lane;
+  const int own = 1 << log_own, tb = t0 + rank * own;
+  constexpr int kWarps = kSkThreads / 32;
+  SkCols cols;
+  SkRow row[2];
+  if (warp >= 2) {
+    load_cols<KIND>(p, n, cols);
+    load_row<KIND>(p, int64_t(tb) + warp, warp < own ? n : p.N, row[0]);
+    load_row<KIND>(p, int64_t(tb) + warp + kWarps, warp + kWarps < own ? n : p.N, row[1]);
+  }
+
+  if (warp == 1) {
+    const uint32_t tmem = *tmem_slot;
+    const bool leader = elect_one();
+    const uint64_t wd0 = sk_desc(smem_u32(sW)), xd0 = sk_desc(smem_u32(sX));
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < nkb; ++i) {
+      const bool got = mbar_wait(&full[stage], phase, wc);
+      if (!__all_sync(0xffffffffu, got)) {
+        *failed = 1;
+        break;
+      }
+      tc_fence_after();
+      if (leader) {
+        const uint64_t wd = wd0 + uint64_t(stage) * (C::W_BYTES >> 4);
+        const uint64_t xd = xd0 + uint64_t(stage) * (C::X_BYTES >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // 32 bytes along K inside the swizzle row
           if constexpr (KIND == kSkBF16)
             mma_bf16(tmem, wd + uint64_t(2 * k), xd + uint64_t(2 * k), sk_idesc<KIND>(NT),
-                     (kb > kb0 || k > 0) ? 1u : 0u);
+                     (i > 0 || k > 0) ? 1u : 0u);
           else
             mma_i8(tmem, wd + uint64_t(2 * k), xd + uint64_t(2 * k), sk_idesc<KIND>(NT),
-                   (kb > kb0 || k > 0) ? 1u : 0u);
+                   (i > 0 || k > 0) ? 1u : 0u);
         }
-        mma_commit(&empty[stage]);
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (i + stages < nkb) mma_commit(&empty[stage]);
       }
-      mma_commit(tfull);  // every MMA issued has completed
-      (void)mbar_wait(tfull, 0, wc);
+      __syncwarp();
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
-  } else {
-    // lane quarter warp % 4 of tensor memory: weight rows 32 q + lane
+    if (leader) mma_commit(tfull);  // every MMA issued has completed
+    __syncwarp();
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp >= 1 && warp < 6) {
     const bool got = mbar_wait(tfull, 0, wc);
-    if (__all_sync(0xffffffffu, got) && !*failed) {
+    if (__all_sync(0xffffffffu, got) && warp >= 2 && !*failed) {
       tc_fence_after();
+      // lane quarter warp % 4 of tensor memory: weight rows 32 q + lane
       const int q = warp & 3;
-      float* dst = part + q * 32 + lane;
+      const uint32_t* dst = recv + (rank << log_own) * kSkRows + q * 32 + lane;
 #pragma unroll
       for (int c = 0; c < NT; c += 32) {
         uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + (uint32_t(q * 32) << 16) + uint32_t(c), r);
+        tmem_ld_32x32b_x32(*tmem_slot + (uint32_t(q * 32) << 16) + uint32_t(c), r);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < NT) dst[(c + i) * kSkRows] = __uint_as_float(r[i]);
+        for (int i = 0; i < 32; ++i) {
+          const int t = c + i;
+          if (t < NT && t0 + t < p.T)
+            st_cluster_u32(mapa_shared(dst + (t & (own - 1)) * kSkRows, uint32_t(t >> log_own)),
+                           r[i]);
+        }
       }
+    } else if (!got) {
+      *failed = 1;
     }
   }
+  if (warp < 2) {
+    load_cols<KIND>(p, n, cols);
+    load_row<KIND>(p, int64_t(tb) + warp, warp < own ? n : p.N, row[0]);
+    load_row<KIND>(p, int64_t(tb) + warp + kWarps, warp + kWarps < own ? n : p.N, row[1]);
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // every CTA's partial sums are in place
+  cluster_sync();  // every CTA's partial sums are with their owners
 
-  if (!*failed) {
-    // this CTA's share of the tokens, a warp a token, four weight rows a lane
-    const int tb = NT * rank / p.split, te = NT * (rank + 1) / p.split;
-    const int n = n0 + 4 * lane;
-    constexpr int kWarps = kSkThreads / 32;
-    for (int tt = tb + warp; tt < te && t0 + tt < p.T; tt += 2 * kWarps) {
-      const int t2 = tt + kWarps < te ? tt + kWarps : tt;
-      const float* s0 = part + tt * kSkRows + 4 * lane;
-      const float* s1 = part + t2 * kSkRows + 4 * lane;
-      uint4 sum[2];
-      if (p.split == 8)
-        join<KIND, 8>(s0, s1, sum);
-      else if (p.split == 4)
-        join<KIND, 4>(s0, s1, sum);
-      else if (p.split == 2)
-        join<KIND, 2>(s0, s1, sum);
-      else
-        join<KIND, 1>(s0, s1, sum);
-      if (n < p.N) {
-        finish4<KIND>(p, sum[0], t0 + tt, n);
-        if (t2 != tt && t0 + t2 < p.T) finish4<KIND>(p, sum[1], t0 + t2, n);
+  if (!*failed && n < p.N) {
+    const uint4* src = reinterpret_cast<const uint4*>(recv) + lane;
+    for (int i = warp; i < own && tb + i < p.T; i += 2 * kWarps) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tt = i + j * kWarps;
+        if (tt < own && tb + tt < p.T) {
+          uint4 sum = src[tt * (kSkRows / 4)];
+#pragma unroll 4
+          for (int k = 1; k < (1 << p.log_split); ++k)
+            add_parts<KIND>(sum, src[((k << log_own) + tt) * (kSkRows / 4)]);
+          finish4<KIND>(p, sum, cols, row[j], int64_t(tb) + tt, n);
+        }
+        load_row<KIND>(p, int64_t(tb) + tt + 2 * kWarps, tt + 2 * kWarps < own ? n : p.N, row[j]);
       }
     }
   }
-  cluster_sync();  // no CTA leaves while a peer may read its partial sums
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc(*tmem_slot, C::TMEM_COLS);
   }
 }
 
 namespace {
 
 template <int KIND, int NT>
-cudaError_t launch_one(const void* tmap_x, const void* tmap_w, const SplitKParams& p, int tiles,
+cudaError_t launch_one(const void* tmap_x, const void* tmap_w, SplitKParams p, int tiles, int sms,
                        cudaStream_t st) {
   using C = SkCfg<NT>;
   const void* fn = (const void*)splitk_kernel<KIND, NT>;
@@ -314,20 +360,26 @@ cudaError_t launch_one(const void* tmap_x, const void* tmap_w, const SplitKParam
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(C::smem(C::STAGES_1)));
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles) * unsigned(p.split));
+  cfg.gridDim = dim3(unsigned(tiles) << p.log_split);
   cfg.blockDim = dim3(kSkThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  // as many stages as K blocks, in the shared memory of an SM where the grid
+  // leaves each CTA one, else of half an SM
+  const int split = 1 << p.log_split;
+  const int most = tiles * split <= sms ? C::STAGES_1 : C::STAGES_2;
+  const int blocks = (p.k_blocks + split - 1) / split;
+  p.stages = blocks > most ? most : blocks;
+  p.log_nt = NT == 16 ? 4 : NT == 32 ? 5 : NT == 64 ? 6 : 7;
+  cfg.dynamicSmemBytes = C::smem(p.stages);
   cfg.stream = st;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = unsigned(p.split);
+  a[0].val.clusterDim.x = 1u << p.log_split;
   a[0].val.clusterDim.y = 1;
   a[0].val.clusterDim.z = 1;
   cfg.attrs = a;
@@ -339,12 +391,12 @@ cudaError_t launch_one(const void* tmap_x, const void* tmap_w, const SplitKParam
 
 template <int KIND>
 cudaError_t launch_nt(int nt, const void* tmap_x, const void* tmap_w, const SplitKParams& p,
-                      int tiles, cudaStream_t st) {
+                      int tiles, int sms, cudaStream_t st) {
   switch (nt) {
-    case 16: return launch_one<KIND, 16>(tmap_x, tmap_w, p, tiles, st);
-    case 32: return launch_one<KIND, 32>(tmap_x, tmap_w, p, tiles, st);
-    case 64: return launch_one<KIND, 64>(tmap_x, tmap_w, p, tiles, st);
-    default: return launch_one<KIND, 128>(tmap_x, tmap_w, p, tiles, st);
+    case 16: return launch_one<KIND, 16>(tmap_x, tmap_w, p, tiles, sms, st);
+    case 32: return launch_one<KIND, 32>(tmap_x, tmap_w, p, tiles, sms, st);
+    case 64: return launch_one<KIND, 64>(tmap_x, tmap_w, p, tiles, sms, st);
+    default: return launch_one<KIND, 128>(tmap_x, tmap_w, p, tiles, sms, st);
   }
 }
 
@@ -356,19 +408,21 @@ SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms) {
   const int64_t tiles = (T + nt - 1) / nt * ((N + kSkRows - 1) / kSkRows);
   const int k_blocks = int((row_bytes + 127) / 128);
   if (tiles > sms / 2) return pl;
-  int split = 8;
-  while (split > 1 && (tiles * split > 2 * sms || split > k_blocks)) split >>= 1;
+  int log_split = 3;
+  while (log_split > 0 && ((tiles << log_split) > 2 * sms || (1 << log_split) > k_blocks))
+    --log_split;
+  pl.use = true;
   pl.nt = nt;
-  pl.split = split;
+  pl.log_split = log_split;
   pl.tiles = int(tiles);
   pl.k_blocks = k_blocks;
   return pl;
 }
 
 cudaError_t launch_splitk(bool bf16, int nt, const void* tmap_x, const void* tmap_w,
-                          const SplitKParams& p, int tiles, cudaStream_t st) {
-  return bf16 ? launch_nt<kSkBF16>(nt, tmap_x, tmap_w, p, tiles, st)
-              : launch_nt<kSkI8>(nt, tmap_x, tmap_w, p, tiles, st);
+                          const SplitKParams& p, int tiles, int sms, cudaStream_t st) {
+  return bf16 ? launch_nt<kSkBF16>(nt, tmap_x, tmap_w, p, tiles, sms, st)
+              : launch_nt<kSkI8>(nt, tmap_x, tmap_w, p, tiles, sms, st);
 }
 
 }  // namespace hq
