@@ -1665,9 +1665,8 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
   if (s != HQ_OK || T == 0) return s;
   if (T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
   // a few tokens: one pass over the weights (the weight-only form's transform
-  // and the raw accumulators need the tiles); without an epilogue the call is
-  // hq_linear whatever T is
-  if (T <= kRowsMaxT && desc->out_order <= 1 && acc_debug == nullptr && !plain_epilogue(epilogue)) {
+  // and the raw accumulators need the tiles)
+  if (T <= kRowsMaxT && desc->out_order <= 1 && acc_debug == nullptr) {
     DeviceState* dev;
     s = device_state(&dev);
     if (s != HQ_OK) return s;
@@ -1692,8 +1691,7 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
                                  reinterpret_cast<cudaStream_t>(stream)));
   }
   // too few tiles for the GPU: K split over a cluster (codes one per byte)
-  if (desc->out_order <= 1 && acc_debug == nullptr && !plain_epilogue(epilogue) &&
-      desc->code_format == HQ_CODES_I8) {
+  if (desc->out_order <= 1 && acc_debug == nullptr && desc->code_format == HQ_CODES_I8) {
     DeviceState* dev;
     s = device_state(&dev);
     if (s != HQ_OK) return s;

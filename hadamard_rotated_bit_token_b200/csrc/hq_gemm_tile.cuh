@@ -899,34 +899,39 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------- MMA issuer
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc_iter = 0;
-      bool ok = true;
-      const uint32_t a_base = smem_u32(sA);
-      const uint32_t b_base = smem_u32(sB);
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++acc_iter) {
-        const int acc = acc_iter & 1;
-        const uint32_t acc_phase = (acc_iter >> 1) & 1;
-        if (*abort_flag || !mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) {
+    // --------------------------------------------------------- MMA issuer
+    // The warp runs the loop converged and one elected thread issues: the loop
+    // itself (barrier tests, descriptors, commits) would otherwise take longer
+    // than the four MMAs of a K block of up to 192 columns.
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc_iter = 0;
+    bool ok = true;
+    const bool leader = elect_one();
+    const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(sA));
+    const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(sB));
+    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++acc_iter) {
+      const int acc = acc_iter & 1;
+      const uint32_t acc_phase = (acc_iter >> 1) & 1;
+      if (!__all_sync(0xffffffffu,
+                      !*abort_flag && mbar_wait(&tempty[acc], acc_phase ^ 1u, wc))) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
+      for (int kb = 0; kb < KB; ++kb) {
+        // B landed (full) and, for packed A, the converters stored A (conv)
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, wc) &&
+                                         (!PK || mbar_wait(&conv[stage], phase, wc)))) {
           *abort_flag = 1;
+          ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
-        for (int kb = 0; kb < KB; ++kb) {
-          // B landed (full) and, for packed A, the converters stored A (conv)
-          if (*abort_flag || !mbar_wait(&full[stage], phase, wc) ||
-              (PK && !mbar_wait(&conv[stage], phase, wc))) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t adesc = sw128_kmajor_desc(a_base + uint32_t(stage) * C::A_BYTES);
-          const uint64_t bdesc = sw128_kmajor_desc(b_base + uint32_t(stage) * C::B_BYTES);
+        if (leader) {
+          const uint64_t adesc = a_desc0 + uint64_t(stage) * (C::A_BYTES >> 4);
+          const uint64_t bdesc = b_desc0 + uint64_t(stage) * (C::B_BYTES >> 4);
 #pragma unroll
           for (int k = 0; k < BK / 32; ++k) {
             // advance 32 bytes along K inside the swizzle row (encoded >> 4)
@@ -938,18 +943,20 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
                              (kb > 0 || k > 0) ? 1u : 0u);
           }
           mma_commit(&empty[stage]);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (kb + 1 == KB) mma_commit(&tfull[acc]);
         }
-        if (!ok) break;
-        mma_commit(&tfull[acc]);
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // wait for every issued MMA before tensor memory can be released
-      mma_commit(drain);
-      (void)mbar_wait(drain, 0, wc);
     }
+    // wait for every issued MMA before tensor memory can be released
+    if (leader) mma_commit(drain);
+    __syncwarp();
+    (void)mbar_wait(drain, 0, wc);
+    __syncwarp();
   } else if (warp < 2 + C::EPW) {
     // ----------------------------------------------------------- epilogue
     const int ew = warp - 2;         // 0 .. EPW - 1
@@ -1250,54 +1257,60 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
       st_shared_cluster_u32(mapa_shared(&issued_by[rank], 0), uint32_t(issued));
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------ MMA issuer (rank 0)
+      // converged, one elected thread issues (see gemm_body)
       int stage = 0;
       uint32_t phase = 0;
       int acc_iter = 0;
       bool ok = true;
-      const uint32_t a_base = smem_u32(sA);
-      const uint32_t b_base = smem_u32(sB);
+      const bool leader = elect_one();
+      const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(sA));
+      const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(sB));
       for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters, ++acc_iter) {
         const int acc = acc_iter & 1;
         const uint32_t acc_phase = (acc_iter >> 1) & 1;
-        if (*abort_flag || !mbar_wait<true>(&tempty[acc], acc_phase ^ 1u, wc)) {
+        if (!__all_sync(0xffffffffu,
+                        !*abort_flag && mbar_wait<true>(&tempty[acc], acc_phase ^ 1u, wc))) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + uint32_t(acc * C::BN);
         for (int kb = 0; kb < KB; ++kb) {
-          if (*abort_flag || !mbar_wait<true>(&full[stage], phase, wc)) {
+          if (!__all_sync(0xffffffffu, mbar_wait<true>(&full[stage], phase, wc))) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t adesc = sw128_kmajor_desc(a_base + uint32_t(stage) * C::A_BYTES);
-          const uint64_t bdesc = sw128_kmajor_desc(b_base + uint32_t(stage) * C::B_BYTES);
+          if (leader) {
+            const uint64_t adesc = a_desc0 + uint64_t(stage) * (C::A_BYTES >> 4);
+            const uint64_t bdesc = b_desc0 + uint64_t(stage) * (C::B_BYTES >> 4);
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k) {
-            // advance 32 bytes along K inside the swizzle row (encoded >> 4)
-            mma_kind_pair<KIND>(d_tmem, adesc + uint64_t(2 * k), bdesc + uint64_t(2 * k), C::IDESC,
-                                (kb > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < BK / 32; ++k) {
+              // advance 32 bytes along K inside the swizzle row (encoded >> 4)
+              mma_kind_pair<KIND>(d_tmem, adesc + uint64_t(2 * k), bdesc + uint64_t(2 * k),
+                                  C::IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+            }
+            mma_commit_pair(&empty[stage], 0x3);
+            if (kb + 1 == KB) mma_commit_pair(&tfull[acc], 0x3);
           }
-          mma_commit_pair(&empty[stage], 0x3);
+          __syncwarp();
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        mma_commit_pair(&tfull[acc], 0x3);
       }
       // every issued MMA completes before either CTA releases its shared
       // memory or tensor memory
-      mma_commit_pair(drain, 0x3);
-      (void)mbar_wait<true>(drain, 0, wc);
-    } else if (lane == 0) {
-      (void)mbar_wait<true>(drain, 0, wc);  // rank 1: the pair's last commit has landed
+      if (leader) mma_commit_pair(drain, 0x3);
+      __syncwarp();
     }
+    // (rank 1: the pair's last commit has landed)
+    (void)mbar_wait<true>(drain, 0, wc);
+    __syncwarp();
   } else {
     // ----------------------------------------------------------- epilogue
     const int ew = warp - 2;         // 0 .. 7

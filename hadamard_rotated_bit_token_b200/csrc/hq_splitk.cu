@@ -75,14 +75,6 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// One thread of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
-               : "=r"(p));
-  return p != 0;
-}
-
 // sum + the partial sums v, per element
 template <int KIND>
 __device__ __forceinline__ void add_parts(uint4& sum, const uint4& v) {

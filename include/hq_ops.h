@@ -70,7 +70,8 @@ typedef struct hq_epilogue {
  *   z[t,n] = s_x[t] * w_scale[n] * acc[t,n] + bias_f32[n] + a_mean[t] * colsum[n],
  * or, in the weight-only Hadamard form, the output-side transform's result
  * plus bias.  Every description, code format and argument of hq_linear;
- * `epilogue` may be NULL (then the call is hq_linear).  N is a multiple of 16
+ * `epilogue` may be NULL (the results are then those of hq_linear, bit for bit).
+ * N is a multiple of 16
  * and T < 2^31 - 256. */
 hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
                        const float* a_scale, const float* a_mean, const int8_t* w_codes,
