@@ -653,7 +653,7 @@ hq_status encode_out_bf16(CUtensorMap* m, const void* base, int64_t rows, int N)
 // only for long main loops over wide N.
 struct GemmChoice {
   bool pair;
-  int bn;  // single-CTA tile width
+  int bn;  // tile width
 };
 
 GemmChoice choose_gemm(int64_t T, int N, int K, int sms, int pair_clusters, int variant,
@@ -688,7 +688,46 @@ GemmChoice choose_gemm(int64_t T, int N, int K, int sms, int pair_clusters, int 
   const int64_t prounds = (ptiles + pair_clusters - 1) / pair_clusters;
   const int64_t srounds = (mt * ((N + best_bn - 1) / best_bn) + sms - 1) / sms;
   const bool pair = kb >= 20 && N % 256 == 0 && prounds <= srounds;
-  return {pair, best_bn};
+  return {pair, pair ? 256 : best_bn};
+}
+
+// The tile of the kernels with an epilogue, and its modelled time in
+// microseconds.  Per tile, in cycles of 1.92 GHz: the K blocks at the rate of
+// shared memory, which every operand byte passes twice (written by the copies,
+// read by the MMAs; the pair halves B's share, and adds its hand-shakes), plus the
+// epilogue's own passes through it; or the epilogue's instructions where those
+// are longer.  Tiles of 256 columns and the pair of that width have the lean
+// epilogue, hidden by long main loops only.  Fitted to sweeps of 512 to 65536
+// tokens over layers of 320 to 4608 inputs and 320 to 8192 outputs in both types
+// (times within about 15 %, the choice within 8 % of the best).
+GemmChoice choose_gemm_ep(int64_t T, int N, int64_t row_bytes, int sms, int pair_clusters,
+                          int logo, bool packed, bool act, double* us_out) {
+  const double kb = double((row_bytes + 127) / 128);
+  GemmChoice best{false, 128};
+  double best_us = 1e30;
+  for (int pair = 0; pair <= 1; ++pair) {
+    if (pair && (pair_clusters <= 0 || logo > 0 || packed)) break;
+    for (int bn : {64, 128, 192, 256}) {
+      if ((pair && bn == 64) || (packed && bn > 192)) continue;
+      const int64_t bm = pair ? 256 : 128;
+      const int64_t tiles = ((T + bm - 1) / bm) * ((N + bn - 1) / bn);
+      const int64_t slots = pair ? pair_clusters : sms;
+      const double rounds = double((tiles + slots - 1) / slots);
+      const double block = pair ? 300.0 + 1.3 * bn : 240.0 + 2.0 * bn;
+      double tile = kb * block + (pair ? 2000.0 : 0.0) + (bn == 256 ? 2500.0 : 14.0 * bn);
+      const double epi = bn == 256 ? (pair ? 16000.0 : 14500.0) : 4000.0 + (act ? 34.0 : 14.0) * bn;
+      if (rounds > 1.0 && tile < epi) tile = epi;  // one tile's is not in the way of the next
+      double us = (rounds * tile + (bn == 256 ? 8000.0 : 1500.0)) / 1920.0;
+      if (us < 1.3 * weights_us(N, row_bytes)) us = 1.3 * weights_us(N, row_bytes);
+      us += rounds > 1.0 ? 4.5 : 3.3;
+      if (us < best_us) {
+        best_us = us;
+        best = GemmChoice{pair != 0, bn};
+      }
+    }
+  }
+  if (us_out) *us_out = best_us;
+  return best;
 }
 
 // Argument checks of hq_quantize_act (description, pointers, alignment);
@@ -793,6 +832,17 @@ hq_status set_epilogue(GemmEpParams* p, const hq_epilogue* ep, const uint16_t* Y
              : HQ_OK;
 }
 
+// Whether hq_rows.cu's one pass over the weights is the faster way.  It always is
+// for one or two tokens; with more its multiply-adds take longer than the tensor
+// cores' fixed cost once the weights pass 24 MB (three or four tokens: 4096 x
+// 4096 in bf16 9.7 us against 8.4) or 8 MB (five to eight: 17.9 against 8.4).
+// Packed codes have no other kernel for few tokens.
+bool few_tokens(int64_t T, int N, int64_t row_bytes, bool packed) {
+  if (T > kRowsMaxT) return false;
+  const int64_t bytes = row_bytes * N;
+  return packed || T <= 2 || bytes <= (T <= 4 ? int64_t(24) << 20 : int64_t(8) << 20);
+}
+
 template <class Params>
 void set_rows_epilogue(Params* p, const hq_epilogue* ep, uint16_t* Y) {
   p->Y = Y;
@@ -819,7 +869,7 @@ hq_status run_splitk(const DeviceState* dev, const SplitKPlan& pl, bool bf16, co
   p->num_n_tiles = (N + 127) / 128;
   p->err = dev->err;
   p->wait_ns = wait_ns();
-  return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, dev->sm_count, st));
+  return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, st));
 }
 
 bool plain_epilogue(const hq_epilogue* ep) {
@@ -863,13 +913,16 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
   const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
   if (variant == HQ_GEMM_CTA_PAIR && clusters_max <= 0 && logo == 0) return HQ_ERR_UNSUPPORTED;
   const GemmChoice gc =
-      choose_gemm(T, N, K, dev->sm_count, clusters_max, variant, logo, packed);
-  const int bn = gc.pair ? 256 : gc.bn;
+      ep != nullptr && variant == HQ_GEMM_AUTO
+          ? choose_gemm_ep(T, N, K, dev->sm_count, clusters_max, logo, packed,
+                           ep->act != HQ_ACT_NONE, nullptr)
+          : choose_gemm(T, N, K, dev->sm_count, clusters_max, variant, logo, packed);
+  const int bn = gc.bn;
   CUtensorMap maps[4];
   CUtensorMap &ta = maps[0], &tb = maps[1], &ty = maps[2];
   s = packed ? encode_packed_a(&ta, a_codes, T, K) : encode_kmajor_i8(&ta, a_codes, T, K, 128);
   if (s != HQ_OK) return s;
-  s = encode_kmajor_i8(&tb, w_codes, N, K, gc.pair ? 128 : bn);
+  s = encode_kmajor_i8(&tb, w_codes, N, K, gc.pair ? bn / 2 : bn);
   if (s != HQ_OK) return s;
   GemmEpParams p;  // the plain kernels take its GemmParams part
   std::memset(&p, 0, sizeof(p));
@@ -903,11 +956,11 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
   p.group_m = kGroupM;
   if (gc.pair) {
     p.num_m_tiles = int((T + 255) / 256);
-    p.num_n_tiles = (N + 255) / 256;
+    p.num_n_tiles = (N + bn - 1) / bn;
     const int64_t tiles = int64_t(p.num_m_tiles) * p.num_n_tiles;
     const int clusters = int(tiles < clusters_max ? tiles : clusters_max);
     if (ep != nullptr)
-      return from_cuda(launch_gemm_pair_ep(false, maps, p, clusters, st));
+      return from_cuda(launch_gemm_pair_ep(false, bn, maps, p, clusters, st));
     return from_cuda(launch_gemm_pair(&ta, &tb, &ty, p, clusters, st));
   }
   p.num_m_tiles = int((T + 127) / 128);
@@ -1666,7 +1719,8 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
   if (T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
   // a few tokens: one pass over the weights (the weight-only form's transform
   // and the raw accumulators need the tiles)
-  if (T <= kRowsMaxT && desc->out_order <= 1 && acc_debug == nullptr) {
+  if (few_tokens(T, desc->N, desc->K, desc->code_format != HQ_CODES_I8) && desc->out_order <= 1 &&
+      acc_debug == nullptr) {
     DeviceState* dev;
     s = device_state(&dev);
     if (s != HQ_OK) return s;
@@ -1696,7 +1750,10 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
     s = device_state(&dev);
     if (s != HQ_OK) return s;
     const SplitKPlan pl = splitk_plan(T, desc->N, desc->K, dev->sm_count);
-    if (pl.use) {
+    double tiles_us;
+    (void)choose_gemm_ep(T, desc->N, desc->K, dev->sm_count, pair_clusters(dev), 0, false,
+                         epilogue != nullptr && epilogue->act != HQ_ACT_NONE, &tiles_us);
+    if (pl.us < tiles_us) {
       SplitKParams p;
       std::memset(&p, 0, sizeof(p));
       p.a_scale = a_scale;
@@ -1735,7 +1792,7 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   if (s != HQ_OK) return s;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int KB = 2 * K;  // bytes per row of X and W
-  if (T <= kRowsMaxT) {  // a few tokens: one pass over W
+  if (few_tokens(T, N, KB, false)) {  // one pass over W
     RowsParams p;
     std::memset(&p, 0, sizeof(p));
     p.A = reinterpret_cast<const uint8_t*>(X);
@@ -1749,19 +1806,21 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
     return from_cuda(launch_rows(0, p, dev->sm_count, st));
   }
   const SplitKPlan pl = splitk_plan(T, N, KB, dev->sm_count);
-  if (pl.use) {  // too few tiles for the GPU
+  double tiles_us;
+  const GemmChoice gc =
+      choose_gemm_ep(T, N, KB, dev->sm_count, pair_clusters(dev), 0, false,
+                     epilogue != nullptr && epilogue->act != HQ_ACT_NONE, &tiles_us);
+  if (pl.us < tiles_us) {  // too few tiles for the GPU
     SplitKParams p;
     std::memset(&p, 0, sizeof(p));
     p.bias16 = bias;
     set_rows_epilogue(&p, epilogue, Y);
     return run_splitk(dev, pl, true, X, T, W, N, KB, &p, st);
   }
-  const GemmChoice gc = choose_gemm(T, N, KB, dev->sm_count, pair_clusters(dev), HQ_GEMM_AUTO, 0,
-                                    false);
-  const int bn = gc.pair ? 256 : gc.bn;
+  const int bn = gc.bn;
   CUtensorMap maps[4];
   if ((s = encode_kmajor_i8(&maps[0], X, T, KB, 128)) != HQ_OK) return s;
-  if ((s = encode_kmajor_i8(&maps[1], W, N, KB, gc.pair ? 128 : bn)) != HQ_OK) return s;
+  if ((s = encode_kmajor_i8(&maps[1], W, N, KB, gc.pair ? bn / 2 : bn)) != HQ_OK) return s;
   GemmEpParams p;
   std::memset(&p, 0, sizeof(p));
   if ((s = set_epilogue(&p, epilogue, Y, T, N, bn, &maps[2], &maps[3])) != HQ_OK) return s;
@@ -1780,7 +1839,7 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   p.num_n_tiles = int(nt);
   if (gc.pair) {
     const int clusters = int(mt * nt < dev->pair_clusters ? mt * nt : dev->pair_clusters);
-    return from_cuda(launch_gemm_pair_ep(true, maps, p, clusters, st));
+    return from_cuda(launch_gemm_pair_ep(true, bn, maps, p, clusters, st));
   }
   const int grid = int(mt * nt < dev->sm_count ? mt * nt : dev->sm_count);
   return from_cuda(launch_gemm_ep(true, bn, 0, false, maps, p, grid, st));

@@ -15,7 +15,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
-  gemm_pair_body<kI8, false>(&tmA, &tmB, &tmY, p);
+  gemm_pair_body<kI8, 256, false>(&tmA, &tmB, &tmY, nullptr, p);
 }
 
 // ------------------------------------------------- tensor-core ceiling
@@ -187,7 +187,7 @@ cudaError_t launch_gemm(int bn, int logo, bool packed_a, const void* tmap_a, con
                   : launch_pk<false>(bn, logo, tmap_a, tmap_b, tmap_y, p, grid, st);
 }
 
-using I8Pair = PairCfg<kI8, false>;
+using I8Pair = PairCfg<kI8, 256, false>;
 
 static cudaError_t configure_pair() {
   static bool configured = false;

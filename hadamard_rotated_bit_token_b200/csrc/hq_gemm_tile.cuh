@@ -51,9 +51,9 @@
 //   loop, so the packed stage costs less shared-memory traffic than an int8
 //   one.  A's stages sit in tensor memory after the two accumulators, so
 //   packed tiles are at most 192 columns wide.
-// gemm_pair_body<KIND, EP>: a cluster of two CTAs per 256 x 256 output tile with
+// gemm_pair_body<KIND, BN, EP>: a cluster of two CTAs per 256 x BN output tile with
 //   the CTA-pair MMA (cta_group::2, M = 256): each CTA loads 128 rows of A and
-//   128 rows of B into its own shared memory, so one SM moves half the B
+//   BN / 2 rows of B into its own shared memory, so one SM moves half the B
 //   bytes per MMA that the single-CTA kernel moves.  Both CTAs' copies
 //   complete on the even CTA's stage barrier, whose producer expects the
 //   bytes of both; the even CTA issues the MMAs and commits to both CTAs.
@@ -1104,20 +1104,24 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
 }
 
 // ---------------------------------------------------------- CTA-pair kernel
-template <int KIND, bool EP>
+// BN: output columns per pair tile (N of each MMA); 256 without EP.
+template <int KIND, int BN, bool EP>
 struct PairCfg {
-  static constexpr int BN = 256;          // output columns per pair tile (N of each MMA)
   static constexpr int BM_PAIR = 2 * BM;  // output rows per pair tile (M of each MMA)
   static constexpr int B_ROWS = BN / 2;   // rows of B each CTA holds
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // per CTA
-  static constexpr int HC = BN / 2;  // columns per epilogue warp
+  static constexpr bool WIDE = EP && kWide<BN>;
+  static constexpr int EPW = WIDE ? BN / 16 : kEpiWarps;  // epilogue warps
+  static constexpr int THREADS = 64 + 32 * EPW;
+  static constexpr int HC = BN * 4 / EPW;  // columns per epilogue warp
   static constexpr int NBOX = EP ? 1 : 2;  // output staging boxes per epilogue warp
-  static constexpr int EPI_STAGE_BYTES = NBOX * kStageBox;
+  static constexpr int EPI_STAGE_BYTES = WIDE ? kEpBox : NBOX * kStageBox;
+  static constexpr int RES_BAR_BYTES = WIDE ? 8 * EPW : 0;
   static constexpr int RING_BYTES = 2 * 3 * BN * 4;
   static constexpr int CTL_BYTES = 512;
-  static constexpr int FIXED = kEpiWarps * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
+  static constexpr int FIXED = EPW * EPI_STAGE_BYTES + RING_BYTES + CTL_BYTES + 1024;
   static constexpr int STAGES_RAW = (kSmemLimit - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   static constexpr int TMEM_COLS = tmem_cols_for(2 * BN);
@@ -1126,7 +1130,7 @@ struct PairCfg {
   static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + FIXED;
   static_assert(B_BYTES % 1024 == 0, "stage bases must stay 1024-byte aligned");
   static_assert(STAGES >= 2, "shared memory budget");
-  static_assert(16 * STAGES + 96 <= CTL_BYTES, "barrier block");
+  static_assert(16 * STAGES + 96 + RES_BAR_BYTES <= CTL_BYTES, "barrier block");
   static_assert(SMEM <= size_t(kSmemLimit), "shared memory budget");
 };
 
@@ -1146,17 +1150,19 @@ struct PairCfg {
 // whose producer then waits until every copy of either CTA has landed: it
 // supplies the missing arrival or cancels the missing bytes of a stage that
 // only one CTA loaded (after a bounded wait gave up).
-template <int KIND, bool EP>
+// tmR: the residual's tensor map, or null (always null without the wide epilogue).
+template <int KIND, int BN, bool EP>
 __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUtensorMap* tmB,
-                                               const CUtensorMap* tmY, const GemmArgs<EP>& p) {
-  using C = PairCfg<KIND, EP>;
+                                               const CUtensorMap* tmY, const CUtensorMap* tmR,
+                                               const GemmArgs<EP>& p) {
+  using C = PairCfg<KIND, BN, EP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sA = smem;
   uint8_t* sB = smem + size_t(C::STAGES) * C::A_BYTES;
   uint8_t* epi_stage = sB + size_t(C::STAGES) * C::B_BYTES;  // 1024-aligned
-  float* ring = reinterpret_cast<float*>(epi_stage + kEpiWarps * C::EPI_STAGE_BYTES);
+  float* ring = reinterpret_cast<float*>(epi_stage + C::EPW * C::EPI_STAGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring) + C::RING_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
@@ -1164,7 +1170,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   uint64_t* pfull = tempty + 2;
   uint64_t* pempty = pfull + 2;
   uint64_t* drain = pempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (wide epilogue)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (C::WIDE ? C::EPW : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued_by = tmem_slot + 2;  // [2], rank 0: stages each CTA loaded
 
@@ -1173,7 +1180,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   const uint32_t rank = cluster_ctarank();
   const WaitCtl wc{p.err, p.wait_ns};
 
-  param_ring_zero<C::BN>(ring, threadIdx.x, kGemmThreads);
+  param_ring_zero<BN>(ring, threadIdx.x, C::THREADS);
   fence_proxy_async_smem();  // the zeros precede the ring's bulk copies
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -1182,11 +1189,13 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);
+      mbar_init(&tempty[a], 2 * C::EPW);
       mbar_init(&pfull[a], 1);
-      mbar_init(&pempty[a], kEpiWarps);
+      mbar_init(&pempty[a], C::EPW);
     }
     mbar_init(drain, 1);
+    if constexpr (C::WIDE)
+      for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
     *abort_flag = 0;
     issued_by[0] = issued_by[1] = 0;
     fence_mbarrier_init();
@@ -1221,7 +1230,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
         const int m_idx = tile_m(p, tile);
         const int n_idx = tile_n(p, tile);
         const int a_row = m_idx * C::BM_PAIR + int(rank) * BM;
-        const int b_row = n_idx * C::BN + int(rank) * C::B_ROWS;
+        const int b_row = n_idx * BN + int(rank) * C::B_ROWS;
         const int a = tiles_issued & 1;
         if (*abort_flag || !mbar_wait(&pempty[a], ((tiles_issued >> 1) & 1) ^ 1u, wc)) {
           *abort_flag = 1;
@@ -1229,9 +1238,9 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
           break;
         }
         if constexpr (KIND == kBF16)
-          param_ring_load16<C::BN>(p, ring + a * 3 * C::BN, n_idx * C::BN, &pfull[a]);
+          param_ring_load16<BN>(p, ring + a * 3 * BN, n_idx * BN, &pfull[a]);
         else
-          param_ring_load<C::BN>(p, ring + a * 3 * C::BN, n_idx * C::BN, &pfull[a]);
+          param_ring_load<BN>(p, ring + a * 3 * BN, n_idx * BN, &pfull[a]);
         ++tiles_issued;
         for (int kb = 0; kb < KB; ++kb) {
           if (*abort_flag || !mbar_wait<true>(&empty[stage], phase ^ 1u, wc)) {
@@ -1276,7 +1285,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + uint32_t(acc * C::BN);
+        const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
         for (int kb = 0; kb < KB; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait<true>(&full[stage], phase, wc))) {
             *abort_flag = 1;
@@ -1313,10 +1322,11 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     __syncwarp();
   } else {
     // ----------------------------------------------------------- epilogue
-    const int ew = warp - 2;         // 0 .. 7
+    const int ew = warp - 2;         // 0 .. EPW - 1
     const int quarter = warp & 3;    // TMEM lanes [32*quarter, 32*quarter + 32)
     const int half = ew >> 2;        // columns [half*HC, half*HC + HC) of the tile
     uint8_t* stg = epi_stage + ew * C::EPI_STAGE_BYTES;
+    [[maybe_unused]] ResStream rs{tmR, rbar + ew, stg, 0, 0};
     const uint32_t tempty0 = mapa_shared(tempty, 0);
     const int row_off = int(rank) * BM + quarter * 32 + lane;
     int acc_iter = 0;
@@ -1325,10 +1335,15 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
       load_row_params(p, int64_t(tile_m(p, cluster_id)) * C::BM_PAIR + row_off, sx_next,
                       mt_next);
     [[maybe_unused]] uint4 res[4];
-    if constexpr (EP) {
+    if constexpr (C::WIDE) {
+      if (tmR && lane == 0 && cluster_id < num_tiles)
+        res_load(p, rs, tile_m(p, cluster_id) * C::BM_PAIR + int(rank) * BM + quarter * 32,
+                 tile_n(p, cluster_id) * BN + half * C::HC);
+    }
+    if constexpr (EP && !C::WIDE) {
       if (cluster_id < num_tiles)
         load_residual(p, int64_t(tile_m(p, cluster_id)) * C::BM_PAIR + row_off,
-                      tile_n(p, cluster_id) * C::BN + half * C::HC, res);
+                      tile_n(p, cluster_id) * BN + half * C::HC, res);
     }
     for (int tile = cluster_id; tile < num_tiles; tile += num_clusters, ++acc_iter) {
       const int acc = acc_iter & 1;
@@ -1337,7 +1352,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
       const int n_idx = tile_n(p, tile);
       EpiTile e;
       e.row0 = m_idx * C::BM_PAIR + int(rank) * BM + quarter * 32;
-      e.col_base = n_idx * C::BN + half * C::HC;
+      e.col_base = n_idx * BN + half * C::HC;
       e.row = int64_t(e.row0) + lane;
       e.row_ok = e.row < p.T;
       e.sx = sx_next;
@@ -1353,7 +1368,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
         break;
       }
       tc_fence_after();
-      const uint32_t t_addr = tmem_base + uint32_t(acc * C::BN + half * C::HC) +
+      const uint32_t t_addr = tmem_base + uint32_t(acc * BN + half * C::HC) +
                               (uint32_t(quarter * 32) << 16);
       auto release_acc = [&] {
         tc_fence_before();
@@ -1368,16 +1383,31 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
         if (lane == 0) mbar_arrive(&pempty[acc]);
       };
       if constexpr (EP) {
-        epi_tile_lean<KIND, C::HC, C::BN, 0>(
-            p, tmY, t_addr, e, gate_row_of(p, e.row), ring + acc * 3 * C::BN, half * C::HC, res,
-            next < num_tiles ? int64_t(tile_m(p, next)) * C::BM_PAIR + row_off : -1,
-            next < num_tiles ? tile_n(p, next) * C::BN + half * C::HC : 0, stg, lane, release_acc,
-            release_params);
+        const int next_row0 =
+            next < num_tiles ? tile_m(p, next) * C::BM_PAIR + int(rank) * BM + quarter * 32 : -1;
+        const int next_col0 = next < num_tiles ? tile_n(p, next) * BN + half * C::HC : 0;
+        if constexpr (C::WIDE) {
+          if (!epi_tile_ep<KIND, BN, 0>(p, tmY, rs, t_addr, e, gate_row_of(p, e.row),
+                                        ring + acc * 3 * BN, half * C::HC, next_row0, next_col0,
+                                        lane, wc, release_acc, release_params)) {
+            *abort_flag = 1;
+            break;
+          }
+        } else {
+          epi_tile_lean<KIND, C::HC, BN, 0>(
+              p, tmY, t_addr, e, gate_row_of(p, e.row), ring + acc * 3 * BN, half * C::HC, res,
+              next_row0 < 0 ? -1 : int64_t(next_row0) + lane, next_col0, stg, lane, release_acc,
+              release_params);
+        }
       } else {
-        epi_tile<C::HC, C::BN, C::NBOX, 0, 3>(p, tmY, t_addr, e,
-                                              ring + acc * 3 * C::BN + half * C::HC, stg, lane,
+        epi_tile<C::HC, BN, C::NBOX, 0, 3>(p, tmY, t_addr, e,
+                                              ring + acc * 3 * BN + half * C::HC, stg, lane,
                                               release_acc, release_params);
       }
+    }
+    if constexpr (C::WIDE) {
+      if (tmR && lane == 0 && rs.used < rs.issued)  // after a give-up: the box in flight lands
+        (void)mbar_wait(rs.bar, rs.used & 1u, wc);
     }
     if (lane == 0) bulk_wait_group<0>();  // all of this warp's stores are complete
     __syncwarp();

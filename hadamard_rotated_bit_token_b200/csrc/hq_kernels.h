@@ -135,13 +135,14 @@ struct GemmEpParams : GemmParams {
 
 // As launch_gemm / launch_gemm_pair.  maps: four CUtensorMap, A and B as there,
 // then Y and the residual (without one: any map) [T,N] bf16 with box {64, 32}
-// and 128-byte swizzle; for bn 256 and the pair Y's box is {32, 32} with 64-byte
-// swizzle and the residual's map is not read.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as
+// and 128-byte swizzle; for bn 256 Y's box is {32, 32} with 64-byte swizzle
+// and the residual's map is not read.  bf16: A and B are bf16 [T, K/2] and [N, K/2] seen as
 // bytes (p.K = bytes per row; logo 0, not packed).  logo 6 takes any bn here.
 cudaError_t launch_gemm_ep(bool bf16, int bn, int logo, bool packed_a, const void* maps,
                            const GemmEpParams& p, int grid, cudaStream_t st);
-cudaError_t launch_gemm_pair_ep(bool bf16, const void* maps, const GemmEpParams& p, int clusters,
-                                cudaStream_t st);
+// The pair: 256 x bn tiles (bn 128, 192 or 256), B's box bn / 2 rows.
+cudaError_t launch_gemm_pair_ep(bool bf16, int bn, const void* maps, const GemmEpParams& p,
+                                int clusters, cudaStream_t st);
 // The packed-code kernels of launch_gemm_ep (hq_gemm_ep_pk.cu).
 cudaError_t launch_gemm_ep_packed(int bn, int logo, const void* maps, const GemmEpParams& p,
                                   int grid, cudaStream_t st);
@@ -198,17 +199,23 @@ struct SplitKParams {
   unsigned int* err;
   unsigned long long wait_ns;
 };
-// nt tokens (16, 32, 64 or 128) per tile, clusters of 2^log_split CTAs; !use:
-// leave it to the tiles.
+// nt tokens (16, 32, 64 or 128) per tile, clusters of 2^log_split CTAs; us: the
+// modelled time (1e30: no plan).
 struct SplitKPlan {
-  bool use;
+  double us;
   int nt, log_split, tiles, k_blocks;
 };
+// Microseconds in which N rows of weights arrive: from L2 what it keeps, at the
+// memory's rate beyond.
+inline double weights_us(int64_t N, int64_t row_bytes) {
+  const double bytes = double(N) * double(row_bytes);
+  return bytes / (bytes > 60e6 ? 6.2e6 : 12e6);
+}
 SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms);
 // tmap_x: [T, row_bytes] as bytes with box {128, nt}; tmap_w: [N, row_bytes]
 // with box {128, 128}; 128-byte swizzle.
 cudaError_t launch_splitk(bool bf16, int nt, const void* tmap_x, const void* tmap_w,
-                          const SplitKParams& p, int tiles, int sms, cudaStream_t st);
+                          const SplitKParams& p, int tiles, cudaStream_t st);
 
 // MMA-only loop (the int8 tensor-core ceiling): `ctas` CTAs (an even number
 // of them in clusters of two when pair), each issuing k_blocks x 4 MMAs of

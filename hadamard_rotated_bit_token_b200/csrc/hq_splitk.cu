@@ -59,16 +59,16 @@ struct SkCfg {
   static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
   static constexpr int RECV_BYTES = NT * kSkRows * 4;  // [split][NT / split][kSkRows]
   static constexpr int CTL_BYTES = 256;
-  // stages for two CTAs an SM (where that leaves three), and for one
-  static constexpr int STAGES_1 = (224 * 1024 - RECV_BYTES) / STAGE_BYTES;
-  static constexpr int STAGES_2 =
-      (110 * 1024 - RECV_BYTES) / STAGE_BYTES >= 3 ? (110 * 1024 - RECV_BYTES) / STAGE_BYTES
-                                                   : STAGES_1;
+  // two CTAs an SM where that leaves three stages (deeper rings gained nothing),
+  // one with 128 tokens
+  static constexpr int STAGES_2 = (110 * 1024 - RECV_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES =
+      STAGES_2 >= 3 ? STAGES_2 : (224 * 1024 - RECV_BYTES) / STAGE_BYTES;
   static constexpr size_t smem(int stages) {
     return size_t(stages) * STAGE_BYTES + RECV_BYTES + CTL_BYTES + 1024;
   }
   static_assert(X_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
-  static_assert(16 * STAGES_1 + 32 <= CTL_BYTES, "barrier block");
+  static_assert(16 * STAGES + 32 <= CTL_BYTES, "barrier block");
 };
 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kSkThreads, 2)
 namespace {
 
 template <int KIND, int NT>
-cudaError_t launch_one(const void* tmap_x, const void* tmap_w, SplitKParams p, int tiles, int sms,
+cudaError_t launch_one(const void* tmap_x, const void* tmap_w, SplitKParams p, int tiles,
                        cudaStream_t st) {
   using C = SkCfg<NT>;
   const void* fn = (const void*)splitk_kernel<KIND, NT>;
@@ -353,19 +353,16 @@ cudaError_t launch_one(const void* tmap_x, const void* tmap_w, SplitKParams p, i
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(C::smem(C::STAGES_1)));
+                             int(C::smem(C::STAGES)));
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles) << p.log_split);
   cfg.blockDim = dim3(kSkThreads);
-  // as many stages as K blocks, in the shared memory of an SM where the grid
-  // leaves each CTA one, else of half an SM
   const int split = 1 << p.log_split;
-  const int most = tiles * split <= sms ? C::STAGES_1 : C::STAGES_2;
   const int blocks = (p.k_blocks + split - 1) / split;
-  p.stages = blocks > most ? most : blocks;
+  p.stages = blocks > C::STAGES ? C::STAGES : blocks;
   p.log_nt = NT == 16 ? 4 : NT == 32 ? 5 : NT == 64 ? 6 : 7;
   cfg.dynamicSmemBytes = C::smem(p.stages);
   cfg.stream = st;
@@ -383,38 +380,49 @@ cudaError_t launch_one(const void* tmap_x, const void* tmap_w, SplitKParams p, i
 
 template <int KIND>
 cudaError_t launch_nt(int nt, const void* tmap_x, const void* tmap_w, const SplitKParams& p,
-                      int tiles, int sms, cudaStream_t st) {
+                      int tiles, cudaStream_t st) {
   switch (nt) {
-    case 16: return launch_one<KIND, 16>(tmap_x, tmap_w, p, tiles, sms, st);
-    case 32: return launch_one<KIND, 32>(tmap_x, tmap_w, p, tiles, sms, st);
-    case 64: return launch_one<KIND, 64>(tmap_x, tmap_w, p, tiles, sms, st);
-    default: return launch_one<KIND, 128>(tmap_x, tmap_w, p, tiles, sms, st);
+    case 16: return launch_one<KIND, 16>(tmap_x, tmap_w, p, tiles, st);
+    case 32: return launch_one<KIND, 32>(tmap_x, tmap_w, p, tiles, st);
+    case 64: return launch_one<KIND, 64>(tmap_x, tmap_w, p, tiles, st);
+    default: return launch_one<KIND, 128>(tmap_x, tmap_w, p, tiles, st);
   }
 }
 
 }  // namespace
 
+// The tile and split of the least modelled time, in microseconds, fitted to
+// sweeps of 4 to 512 tokens over layers of 256 to 4608 inputs and 1152 to 16384
+// outputs in both types: a launch and its barriers, 0.2 a K block (no faster
+// than the weights arrive), 0.03 a token for the exchange and 0.055 for each that
+// a CTA owns; stretched once the grid passes one CTA an SM.
 SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms) {
-  SplitKPlan pl = {};
-  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  const int64_t tiles = (T + nt - 1) / nt * ((N + kSkRows - 1) / kSkRows);
+  SplitKPlan best = {};
+  best.us = 1e30;
   const int k_blocks = int((row_bytes + 127) / 128);
-  if (tiles > sms / 2) return pl;
-  int log_split = 3;
-  while (log_split > 0 && ((tiles << log_split) > 2 * sms || (1 << log_split) > k_blocks))
-    --log_split;
-  pl.use = true;
-  pl.nt = nt;
-  pl.log_split = log_split;
-  pl.tiles = int(tiles);
-  pl.k_blocks = k_blocks;
-  return pl;
+  const double arrive = weights_us(N, row_bytes);
+  for (int nt : {16, 32, 64, 128}) {
+    if (nt > 16 && nt >= 2 * T) break;
+    const int64_t tiles = (T + nt - 1) / nt * ((N + kSkRows - 1) / kSkRows);
+    for (int ls = 0; ls <= 3 && (1 << ls) <= k_blocks; ++ls) {
+      if ((tiles << ls) > 4 * int64_t(sms)) break;
+      double f = double(tiles << ls) / sms;
+      if (f < 1.0) f = 1.0;
+      // one CTA an SM: clusters of four or eight leave some SMs without one
+      if (nt == 128 && ls >= 2 && (tiles << ls) > sms * 4 / 5) f = 2.0;
+      double product = 0.2 * ((k_blocks >> ls) + 1) * f;
+      if (product < arrive) product = arrive;
+      const double us = 3.9 + product + (0.03 * nt + 0.055 * (nt >> ls)) * f;
+      if (us < best.us) best = SplitKPlan{us, nt, ls, int(tiles), k_blocks};
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_splitk(bool bf16, int nt, const void* tmap_x, const void* tmap_w,
-                          const SplitKParams& p, int tiles, int sms, cudaStream_t st) {
-  return bf16 ? launch_nt<kSkBF16>(nt, tmap_x, tmap_w, p, tiles, sms, st)
-              : launch_nt<kSkI8>(nt, tmap_x, tmap_w, p, tiles, sms, st);
+                          const SplitKParams& p, int tiles, cudaStream_t st) {
+  return bf16 ? launch_nt<kSkBF16>(nt, tmap_x, tmap_w, p, tiles, st)
+              : launch_nt<kSkI8>(nt, tmap_x, tmap_w, p, tiles, st);
 }
 
 }  // namespace hq
