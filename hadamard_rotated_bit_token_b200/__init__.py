@@ -137,8 +137,7 @@ class Epilogue(ctypes.Structure):
     def __init__(self, act=HQ_ACT_NONE, residual=None, gate=None, gate_rows=0):
         if gate is not None and gate_rows < 1:
             raise ValueError("a gate needs gate_rows >= 1 (rows of Y per row of the gate)")
-        super().__init__(act, None if residual is None else _ptr(residual),
-                         None if gate is None else _ptr(gate), gate_rows)
+        super().__init__(act, _ptr(residual), _ptr(gate), gate_rows)
         self.residual, self.gate = residual, gate
 
 
@@ -467,12 +466,39 @@ def hq_gw_debug_linear_f32(desc: GwDesc, a_codes, a_scale, u, w_codes, w_scale, 
 # These check dtypes, shapes and devices, and run on the tensors' device (its
 # current stream when none is given), whichever device is current.
 
+class _Runtime:
+    """What every call of these needs, looked up once: a small call's time on
+    the host is longer than on the device."""
+
+    def __init__(self):
+        import torch
+        lib = load_library()
+        self.bf16, self.f32, self.i8 = torch.bfloat16, torch.float32, torch.int8
+        self.u8, self.i32 = torch.uint8, torch.int32
+        self.device_guard = torch.cuda.device
+        self.current_device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream_of = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        self.dense, self.linear_ep, self.group_norm = (lib.hq_dense, lib.hq_linear_ep,
+                                                       lib.hq_group_norm)
+
+
+_rt = None
+
+
+def _runtime():
+    global _rt
+    if _rt is None:
+        _rt = _Runtime()
+    return _rt
+
+
 def _tensor(t, name, dtype, shape, dev):
     """The address of a contiguous CUDA tensor of this dtype, shape and device
     index (None stays None)."""
     if t is None:
         return None
-    if (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+    if (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
         return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{name} must live on CUDA device {dev}, got {t.device}")
@@ -490,70 +516,65 @@ def _device_of(t, name):
     return dev
 
 
-def _launch(dev, stream, call, where):
-    """call(stream handle) with device `dev` current."""
-    import torch
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            return _launch(dev, stream, call, where)
+def _launch(rt, dev, stream, where, fn, *args):
+    """fn(*args, stream handle) with device `dev` current."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = rt.stream_of(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    status = call(stream)
+    if rt.current_device() != dev:
+        with rt.device_guard(dev):
+            status = fn(*args, stream)
+    else:
+        status = fn(*args, stream)
     if status:
         _check(status, where)
 
 
-def _epilogue_ref(ep, T, N, dev):
+def _epilogue_ref(rt, ep, T, N, dev):
     """By-reference argument of an Epilogue (or None) for a [T, N] output."""
-    import torch
     if ep is None:
         return None
     if ep.residual is not None:
-        _tensor(ep.residual, "residual", torch.bfloat16, (T, N), dev)
+        ep._residual = _tensor(ep.residual, "residual", rt.bf16, (T, N), dev)
     if ep.gate is not None:
-        _tensor(ep.gate, "gate", torch.bfloat16, (-(-T // ep.gate_rows), N), dev)
+        if ep.gate_rows < 1:
+            raise ValueError("a gate needs gate_rows >= 1 (rows of Y per row of the gate)")
+        ep._gate = _tensor(ep.gate, "gate", rt.bf16, (-(-T // ep.gate_rows), N), dev)
     return ctypes.byref(ep)
 
 
 def hq_linear_ep(desc: LayerDesc, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
                  epilogue, Y, acc_debug=None, stream=None):
-    """hq_linear with an Epilogue (None: hq_linear itself)."""
-    import torch
-    f32, T, K, N = torch.float32, a_codes.shape[0], desc.K, desc.N
+    """hq_linear with an Epilogue (None: the results of hq_linear)."""
+    rt = _rt or _runtime()
+    f32, T, K, N = rt.f32, a_codes.shape[0], desc.K, desc.N
     dev = _device_of(a_codes, "a_codes")
     if desc.code_format == HQ_CODES_I4_PACKED:
-        a = _tensor(a_codes, "a_codes", torch.uint8, (T, K // 2), dev)
+        a = _tensor(a_codes, "a_codes", rt.u8, (T, K // 2), dev)
     else:
-        a = _tensor(a_codes, "a_codes", torch.int8, (T, K), dev)
-    sx = _tensor(a_scale, "a_scale", f32, (T if desc.act_gran == HQ_PER_TOKEN else 1,), dev)
-    m = _tensor(a_mean, "a_mean", f32, (T,), dev)
-    w = _tensor(w_codes, "w_codes", torch.int8, (N, K), dev)
-    sw = _tensor(w_scale, "w_scale", f32, (N,), dev)
-    cs = _tensor(colsum, "colsum", f32, (N,), dev)
-    b = _tensor(bias_f32, "bias_f32", f32, (N,), dev)
-    y = _tensor(Y, "Y", torch.bfloat16, (T, N), dev)
-    acc = _tensor(acc_debug, "acc_debug", torch.int32, (T, N), dev)
-    ep = _epilogue_ref(epilogue, T, N, dev)
-    fn = load_library().hq_linear_ep
-    _launch(dev, stream, lambda st: fn(ctypes.byref(desc), T, a, sx, m, w, sw, cs, b, ep, y, acc,
-                                       st), "hq_linear_ep")
+        a = _tensor(a_codes, "a_codes", rt.i8, (T, K), dev)
+    n = (N,)
+    _launch(rt, dev, stream, "hq_linear_ep", rt.linear_ep, ctypes.byref(desc), T, a,
+            _tensor(a_scale, "a_scale", f32, (T,) if desc.act_gran == HQ_PER_TOKEN else (1,), dev),
+            _tensor(a_mean, "a_mean", f32, (T,), dev),
+            _tensor(w_codes, "w_codes", rt.i8, (N, K), dev),
+            _tensor(w_scale, "w_scale", f32, n, dev), _tensor(colsum, "colsum", f32, n, dev),
+            _tensor(bias_f32, "bias_f32", f32, n, dev), _epilogue_ref(rt, epilogue, T, N, dev),
+            _tensor(Y, "Y", rt.bf16, (T, N), dev),
+            _tensor(acc_debug, "acc_debug", rt.i32, (T, N), dev))
 
 
 def hq_dense(desc: DenseDesc, X, W, bias, epilogue, Y, stream=None):
     """Y = residual + gate * act(X W^T + bias) in bf16 (epilogue None: the
     product plus bias)."""
-    import torch
-    bf16, T = torch.bfloat16, X.shape[0]
+    rt = _rt or _runtime()
+    bf16, T, K, N = rt.bf16, X.shape[0], desc.K, desc.N
     dev = _device_of(X, "X")
-    x = _tensor(X, "X", bf16, (T, desc.K), dev)
-    w = _tensor(W, "W", bf16, (desc.N, desc.K), dev)
-    b = _tensor(bias, "bias", bf16, (desc.N,), dev)
-    y = _tensor(Y, "Y", bf16, (T, desc.N), dev)
-    ep = _epilogue_ref(epilogue, T, desc.N, dev)
-    fn = load_library().hq_dense
-    _launch(dev, stream, lambda st: fn(ctypes.byref(desc), x, T, w, b, ep, y, st), "hq_dense")
+    _launch(rt, dev, stream, "hq_dense", rt.dense, ctypes.byref(desc),
+            _tensor(X, "X", bf16, (T, K), dev), T, _tensor(W, "W", bf16, (N, K), dev),
+            _tensor(bias, "bias", bf16, (N,), dev), _epilogue_ref(rt, epilogue, T, N, dev),
+            _tensor(Y, "Y", bf16, (T, N), dev))
 
 
 def hq_group_norm_workspace_bytes(desc: GroupNormDesc, B: int, S: int) -> int:
@@ -563,27 +584,20 @@ def hq_group_norm_workspace_bytes(desc: GroupNormDesc, B: int, S: int) -> int:
 def hq_group_norm(desc: GroupNormDesc, X, gamma, beta, Y, workspace=None, stream=None):
     """Y = act(group norm of X) over channels-last X [B, ..., C]; workspace: a
     uint8 tensor of hq_group_norm_workspace_bytes(desc, B, S) bytes (S: the
-    product of the dimensions between) where that is not 0."""
-    import torch
-    bf16, C = torch.bfloat16, desc.C
-    if X.dim() < 2 or X.shape[-1] != C:
-        raise ValueError(f"X must have shape [B, ..., {C}], got {tuple(X.shape)}")
+    product of the dimensions between)."""
+    rt = _rt or _runtime()
+    bf16, C, shape = rt.bf16, desc.C, X.shape
+    if len(shape) < 2 or shape[-1] != C:
+        raise ValueError(f"X must have shape [B, ..., {C}], got {tuple(shape)}")
     dev = _device_of(X, "X")
-    B = X.shape[0]
     S = 1
-    for n in X.shape[1:-1]:
+    for n in shape[1:-1]:
         S *= n
-    x = _tensor(X, "X", bf16, X.shape, dev)
-    g = _tensor(gamma, "gamma", bf16, (C,), dev)
-    b = _tensor(beta, "beta", bf16, (C,), dev)
-    y = _tensor(Y, "Y", bf16, X.shape, dev)
-    ws, nws = None, 0
-    if workspace is not None:
-        nws = workspace.numel()
-        ws = _tensor(workspace, "workspace", torch.uint8, (nws,), dev)
-    fn = load_library().hq_group_norm
-    _launch(dev, stream, lambda st: fn(ctypes.byref(desc), x, B, S, g, b, y, ws, nws, st),
-            "hq_group_norm")
+    nws = 0 if workspace is None else workspace.numel()
+    _launch(rt, dev, stream, "hq_group_norm", rt.group_norm, ctypes.byref(desc),
+            _tensor(X, "X", bf16, shape, dev), shape[0], S, _tensor(gamma, "gamma", bf16, (C,), dev),
+            _tensor(beta, "beta", bf16, (C,), dev), _tensor(Y, "Y", bf16, shape, dev),
+            _tensor(workspace, "workspace", rt.u8, (nws,), dev), nws)
 
 
 # ---------------------------------------------------------------------------
@@ -877,22 +891,42 @@ class GroupWiseQuantLinear:
 
 
 class DenseLinear:
-    """A linear layer in 16 bits (hq_dense): weight bf16 [N, K], bias bf16 [N]
-    or None, and an activation (HQ_ACT_*)."""
+    """A linear layer in 16 bits (hq_dense): weight bf16 [N, K] and bias bf16
+    [N] or None, fixed at construction (their values may change in place), and
+    an activation (HQ_ACT_*)."""
 
     def __init__(self, weight, bias=None, act=HQ_ACT_NONE):
-        self.weight, self.bias, self.act = weight, bias, act
-        self.desc = DenseDesc(weight.shape[1], weight.shape[0])
+        if weight.dim() != 2:
+            raise ValueError(f"weight must have shape [N, K], got {tuple(weight.shape)}")
+        N, K = weight.shape
+        rt = _runtime()
+        self._dev = _device_of(weight, "weight")
+        _tensor(weight, "weight", rt.bf16, (N, K), self._dev)
+        _tensor(bias, "bias", rt.bf16, (N,), self._dev)
+        self._weight, self._bias, self.act = weight, bias, act
+        self.desc = DenseDesc(K, N)
+        self._ref = ctypes.byref(self.desc)
+
+    weight = property(lambda self: self._weight)
+    bias = property(lambda self: self._bias)
 
     def forward(self, X, Y=None, residual=None, gate=None, gate_rows=0):
         """X bf16 [T, K] -> Y [T, N] = residual + gate[t // gate_rows] * act(X W^T + b)."""
-        import torch
+        rt, dev, w = _rt, self._dev, self._weight
+        N, K = w.shape
+        T = X.shape[0]
+        x = _tensor(X, "X", rt.bf16, (T, K), dev)
         if Y is None:
-            Y = torch.empty((X.shape[0], self.desc.N), dtype=torch.bfloat16, device=X.device)
+            Y = X.new_empty((T, N))
+            y = Y.data_ptr()
+        else:
+            y = _tensor(Y, "Y", rt.bf16, (T, N), dev)
         ep = None
-        if self.act != HQ_ACT_NONE or residual is not None or gate is not None:
-            ep = Epilogue(self.act, residual, gate, gate_rows)
-        hq_dense(self.desc, X, self.weight, self.bias, ep, Y)
+        if self.act or residual is not None or gate is not None:
+            ep = _epilogue_ref(rt, Epilogue(self.act, residual, gate, gate_rows), T, N, dev)
+        b = self._bias
+        _launch(rt, dev, None, "hq_dense", rt.dense, self._ref, x, T, w.data_ptr(),
+                None if b is None else b.data_ptr(), ep, y)
         return Y
 
     __call__ = forward
@@ -905,21 +939,27 @@ class GroupNorm:
     def __init__(self, channels, groups, gamma=None, beta=None, eps=1e-5, act=HQ_ACT_NONE):
         self.desc = GroupNormDesc(channels, groups, act, eps)
         self.gamma, self.beta = gamma, beta
+        self._ws_bytes = {}
 
     def forward(self, X, Y=None):
         """X bf16 [B, ..., C] -> Y of the same shape (Y may be X).  The
         workspace comes from PyTorch's allocator at every call, on the current
         stream, so calls on several streams share none."""
-        import torch
+        rt = _rt or _runtime()
         if Y is None:
-            Y = torch.empty_like(X)
-        B, C = X.shape[0], self.desc.C
-        n = X.numel()
-        ws = None
+            Y = X.new_empty(X.shape)
+        ws, n = None, X.numel()
         if n:
-            nb = hq_group_norm_workspace_bytes(self.desc, B, n // (B * C))
-            if nb:
-                ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
+            key = (X.get_device(), X.shape[0], n)
+            nb = self._ws_bytes.get(key)
+            if nb is None:
+                if key[0] < 0 or X.shape[-1] != self.desc.C:
+                    return hq_group_norm(self.desc, X, self.gamma, self.beta, Y)  # refuses X
+                with rt.device_guard(key[0]):
+                    nb = hq_group_norm_workspace_bytes(self.desc, key[1],
+                                                       n // (key[1] * self.desc.C))
+                self._ws_bytes[key] = nb
+            ws = X.new_empty(nb, dtype=rt.u8)
         hq_group_norm(self.desc, X, self.gamma, self.beta, Y, ws)
         return Y
 

@@ -408,8 +408,10 @@ SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms) {
       if ((tiles << ls) > 4 * int64_t(sms)) break;
       double f = double(tiles << ls) / sms;
       if (f < 1.0) f = 1.0;
-      // one CTA an SM: clusters of four or eight leave some SMs without one
-      if (nt == 128 && ls >= 2 && (tiles << ls) > sms * 4 / 5) f = 2.0;
+      // one CTA an SM, and clusters of four or eight leave some SMs without one:
+      // whole waves
+      const int64_t at_once = ls >= 2 ? int64_t(sms) * 6 / 7 : sms;
+      if (nt == 128) f = double(((tiles << ls) + at_once - 1) / at_once);
       double product = 0.2 * ((k_blocks >> ls) + 1) * f;
       if (product < arrive) product = arrive;
       const double us = 3.9 + product + (0.03 * nt + 0.055 * (nt >> ls)) * f;
