@@ -575,7 +575,10 @@ __device__ __forceinline__ bool epi_tile_ep(const GemmEpParams& p, const CUtenso
     if (lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
   }
-  if constexpr (LOGO < 6) {
+  if (e.row0 >= p.T || e.col_base >= p.N) {  // nothing of Y here
+    release_acc();
+    release_params();
+  } else if constexpr (LOGO < 6) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       uint32_t r[32];
@@ -692,8 +695,17 @@ __device__ __forceinline__ void epi_tile_lean(const GemmEpParams& p, const CUten
     epi_store_chunk(p, tmY, packed, col, e.row0, box, lane);
   };
   constexpr int G = LOGO == 6 ? 2 : 1;
+  // chunks past Y's last column are left out, all of them below its last row
+  const int live = e.row0 >= p.T || e.col_base >= p.N ? 0 : (p.N - e.col_base + 31) / 32;
 #pragma unroll 1
   for (int c0 = 0; c0 < NCH; c0 += G) {
+    if (c0 >= live) {
+      // (next tile's residual: the last live chunk has not asked for it)
+      if (p.residual != nullptr && next_row >= 0) load_residual(p, next_row, next_col, res);
+      release_acc();
+      release_params();
+      return;
+    }
     f2 z[G][16];
 #pragma unroll
     for (int c = 0; c < G; ++c) {

@@ -263,7 +263,10 @@ __global__ void __launch_bounds__(kGnThreads, 1) gn_stats_kernel(const GnParams 
   const int nv = p.nv, RP = p.RP;
   // passes over slices of p.gs whole groups, at most kGnThreads vectors a row;
   // a single group may be wider: its row is then walked by all threads
-  for (int g0 = 0; g0 < p.G; g0 += p.gs) {
+  for (int g1 = 0; g1 < p.G; g1 += p.gs) {
+    // (the last pass starts early enough to be a whole one: the groups it shares
+    // with the one before come out the same)
+    const int g0 = min(g1, p.G - p.gs);
     const uint16_t* xs = base + g0 * p.cpg;
     if (nv <= kGnThreads) {
       const int rp = div_small(int(threadIdx.x), p.magic_nv), cv = int(threadIdx.x) - rp * nv;
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kGnThreads, 1) gn_stats_kernel(const GnParams 
                              rem * VEC, float(rows) * float(q + 1), float(rows) * float(q),
                              outp + g0);
     }
-    if (g0 + p.gs < p.G) __syncthreads();
+    if (g1 + p.gs < p.G) __syncthreads();
   }
 }
 
@@ -496,9 +499,12 @@ void gn_plan(GnParams* p, int* vec, int sms) {
     const int unit = v / gcd(cpg, v);
     if (unit > 1 && int64_t(unit) * cpg / v > kGnThreads) continue;
     *vec = v;
-    p->gs = unit;
-    for (int gs = unit; gs <= G && int64_t(gs) * cpg / v <= kGnThreads; gs += unit)
-      if (G % gs == 0) p->gs = gs;
+    // as few passes as fit, of equal size up to the vectors' unit
+    const int units = G / unit;
+    int per = int(int64_t(kGnThreads) * v / (int64_t(unit) * cpg));
+    per = per < 1 ? 1 : per > units ? units : per;
+    const int passes = (units + per - 1) / per;
+    p->gs = (units + passes - 1) / passes * unit;
     break;
   }
   int64_t want = sms / p->B;

@@ -57,6 +57,9 @@ DENSE_SHAPES = [
     (17, 136, 1144), (33, 64, 128), (64, 4608, 1152), (65, 1152, 136), (127, 200, 328),
     (128, 128, 256), (129, 1160, 776), (257, 4096, 512), (1000, 2600, 1160), (2049, 320, 320),
     (300, 8, 2048), (4100, 1152, 1152),
+    # few tokens and narrow layers: every split and token tile of the K split
+    (5, 4096, 4096), (9, 64, 128), (10, 192, 136), (24, 8192, 512), (31, 320, 1000),
+    (48, 2304, 3456), (96, 1600, 144), (200, 4608, 264), (400, 72, 72), (12, 15000, 8),
 ]
 
 
@@ -164,6 +167,48 @@ def test_dense_in_place_residual_and_determinism(hq, T):
     assert hq.hq_check_device_error() == 0
 
 
+@pytest.mark.parametrize("T", [1, 4, 40, 130, 1500])
+def test_linear_ep_in_place_residual(hq, T):
+    """Added in place, on every code format, again and again the same bits."""
+    K, N = 544, 720
+    g = _gen(T)
+    A, W = _codes(g, T, K, 4), _codes(g, N, K, 4)
+    sx, sw, b = torch.rand(T, generator=g, device="cuda"), torch.rand(
+        N, generator=g, device="cuda") * 0.01, _randn(g, N)
+    R = _bf(_randn(g, T, N))
+    for fmt, codes in ((hq.HQ_CODES_I8, A), (hq.HQ_CODES_I4_PACKED, pack_i4(A))):
+        desc = hq.LayerDesc(K, N, 16, code_format=fmt)
+        Y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+        hq.hq_linear_ep(desc, codes, sx, None, W, sw, None, b, hq.Epilogue(SILU, R), Y)
+        for _ in range(3):
+            Z = R.clone()
+            hq.hq_linear_ep(desc, codes, sx, None, W, sw, None, b, hq.Epilogue(SILU, Z), Z)
+            assert torch.equal(Y, Z)
+    assert hq.hq_check_device_error() == 0
+
+
+def test_products_on_two_streams_at_once(hq):
+    """Many calls of every kernel kind in flight on two streams."""
+    g = _gen(12)
+    cases = []
+    for T, K, N in ((1, 1152, 1152), (8, 512, 640), (30, 2304, 1152), (200, 1152, 1152),
+                    (3000, 1152, 1152)):
+        X, W = _bf(_randn(g, T, K)), _bf(_randn(g, N, K) * 0.03)
+        layer = hq.DenseLinear(W, None, GELU)
+        cases.append((layer, X, layer(X)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for i in range(6):
+        for layer, X, want in cases:
+            for st in streams:
+                with torch.cuda.stream(st):
+                    outs.append((layer(X), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+    assert hq.hq_check_device_error() == 0
+
+
 def test_dense_gate_rows_cross_tiles(hq):
     """Gate rows of every length against tiles of 128 rows."""
     K, N, T = 64, 96, 515
@@ -257,7 +302,9 @@ def _linear_case(hq, T, K, N, a_bits, w_bits, act, per_token=True, mean=True, pa
 
 LINEAR_SHAPES = [(1, 16, 16), (1, 1152, 3456), (2, 4608, 1152), (5, 80, 48), (17, 1040, 272),
                  (40, 320, 320), (64, 1152, 1168), (100, 2048, 336), (129, 144, 640),
-                 (300, 1024, 1024), (1025, 2560, 512), (2000, 320, 320)]
+                 (300, 1024, 1024), (1025, 2560, 512), (2000, 320, 320), (9, 16, 16),
+                 (12, 8192, 128), (30, 1040, 3456), (90, 4608, 272), (250, 208, 144),
+                 (4100, 640, 1152), (600, 8192, 1536)]
 
 
 @pytest.mark.parametrize("T,K,N", LINEAR_SHAPES)
@@ -271,7 +318,7 @@ def test_linear_ep(hq, T, K, N, form):
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 32, 16), (1, 1152, 3456), (7, 1056, 272), (200, 320, 336),
-                                   (1025, 2560, 512)])
+                                   (1025, 2560, 512), (12, 64, 32), (3000, 1152, 1152)])
 @pytest.mark.parametrize("a_bits", [3, 4])
 def test_linear_ep_packed(hq, T, K, N, a_bits):
     _linear_case(hq, T, K, N, a_bits, 4, SILU, packed=True, residual=True, rows=max(1, T - 1))
@@ -303,16 +350,17 @@ def test_linear_ep_extreme_codes(hq):
 
 def test_linear_ep_plain_equals_linear(hq):
     """Without activation, gate and residual the call is hq_linear, bit for bit."""
-    T, K, N = 300, 1152, 1152
-    g = _gen(1)
-    A, W = _codes(g, T, K, 4), _codes(g, N, K, 4)
-    sx, sw, b, m, cs = (_randn(g, n).abs() for n in (T, N, N, T, N))
-    desc = hq.LayerDesc(K, N, 128)
-    Y = [torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
-    hq.hq_linear(desc, A, sx, m, W, sw, cs, b, Y[0])
-    hq.hq_linear_ep(desc, A, sx, m, W, sw, cs, b, None, Y[1])
-    hq.hq_linear_ep(desc, A, sx, m, W, sw, cs, b, hq.Epilogue(), Y[2])
-    assert torch.equal(Y[0], Y[1]) and torch.equal(Y[0], Y[2])
+    K, N = 1152, 1152
+    for T in (1, 6, 40, 300, 3000):
+        g = _gen(T)
+        A, W = _codes(g, T, K, 4), _codes(g, N, K, 4)
+        sx, sw, b, m, cs = (_randn(g, n).abs() for n in (T, N, N, T, N))
+        desc = hq.LayerDesc(K, N, 128)
+        Y = [torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        hq.hq_linear(desc, A, sx, m, W, sw, cs, b, Y[0])
+        hq.hq_linear_ep(desc, A, sx, m, W, sw, cs, b, None, Y[1])
+        hq.hq_linear_ep(desc, A, sx, m, W, sw, cs, b, hq.Epilogue(), Y[2])
+        assert torch.equal(Y[0], Y[1]) and torch.equal(Y[0], Y[2])
 
 
 def test_layer_with_epilogue_in_a_graph(hq):
@@ -343,6 +391,10 @@ GN_SHAPES = [  # B, S, C, G
     (1, 513, 12, 1), (2, 100, 2560, 32), (1, 31, 8192, 32), (1, 3, 8190, 7), (5, 64, 96, 96),
     (1, 20000, 128, 32), (1, 9000, 64, 1), (300, 16, 64, 8), (1, 7001, 30, 3), (70000, 1, 16, 2),
     (1, 5000, 36, 9), (16, 4096, 320, 32),
+    # prime numbers of groups (passes that overlap), one channel a group, wide rows
+    (1, 64, 8191, 8191), (2, 40, 1021, 1021), (1, 300, 5160, 1290), (2, 17, 6186, 1031),
+    (3, 9, 8184, 8184), (1, 50, 4104, 8), (1, 12, 8192, 1), (1, 700, 8191, 1), (149, 2, 40, 4),
+    (5, 1031, 8, 8),
 ]
 
 
