@@ -464,7 +464,8 @@ def hq_gw_debug_linear_f32(desc: GwDesc, a_codes, a_scale, u, w_codes, w_scale, 
 # the operators beside the layer (include/hq_ops.h), same names
 # ---------------------------------------------------------------------------
 # These check dtypes, shapes and devices, and run on the tensors' device (its
-# current stream when none is given), whichever device is current.
+# current stream when none is given), whichever device is current.  Like the
+# layer they are for inference: no gradient is recorded.
 
 class _Runtime:
     """What every call of these needs, looked up once: a small call's time on

@@ -794,6 +794,7 @@ bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
 }
 
 constexpr int64_t kMaxEpRows = (int64_t(1) << 31) - 256;  // row coordinates are int32
+constexpr int kMaxEpCols = 1 << 30;                       // and so are columns, tiles past N too
 
 bool known_act(int act) { return act >= HQ_ACT_NONE && act <= HQ_ACT_GELU_TANH; }
 
@@ -1716,7 +1717,7 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
                                   bias_f32, Y, acc_debug);
   if (s == HQ_OK) s = check_epilogue(epilogue, T, desc->N, Y);
   if (s != HQ_OK || T == 0) return s;
-  if (T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
+  if (T > kMaxEpRows || desc->N > kMaxEpCols) return HQ_ERR_UNSUPPORTED;
   // a few tokens: one pass over the weights (the weight-only form's transform
   // and the raw accumulators need the tiles)
   if (few_tokens(T, desc->N, desc->K, desc->code_format != HQ_CODES_I8) && desc->out_order <= 1 &&
@@ -1776,7 +1777,8 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
                    hq_stream_t stream) {
   if (desc == nullptr || T < 0 || desc->K <= 0 || desc->N <= 0) return HQ_ERR_INVALID_ARGUMENT;
   const int K = desc->K, N = desc->N;
-  if (K % 8 != 0 || N % 8 != 0 || K > (1 << 20) || T > kMaxEpRows) return HQ_ERR_UNSUPPORTED;
+  if (K % 8 != 0 || N % 8 != 0 || K > (1 << 20) || N > kMaxEpCols || T > kMaxEpRows)
+    return HQ_ERR_UNSUPPORTED;
   hq_status s = check_epilogue(epilogue, T, N, Y);
   if (s != HQ_OK || T == 0) return s;
   if (X == nullptr || W == nullptr || Y == nullptr) return HQ_ERR_INVALID_ARGUMENT;

@@ -489,11 +489,15 @@ __device__ __forceinline__ void epi_tile(const GemmParams& p, const CUtensorMap*
 //   lean (256 columns and the CTA pair): eight warps of 128 columns with one
 //     32 x 32 box each, so that the operands keep four stages of 48 KB (six of
 //     32 KB in the pair); R comes from global memory into registers one chunk
-//     ahead.  For long main loops: 16384 x 4096 x 8192 in bf16 takes 764 us so,
-//     843 us with sixteen warps and four stages.
+//     ahead.  For long main loops: 16384 x 4096 x 8192 in bf16 takes 742-800 us
+//     so (the clock under load varies), 843-869 us with sixteen warps, 64 KB of
+//     boxes and four stages.  In between, 16384 x 1152 x 4608 in bf16: 134 us by
+//     the lean pair, 148 by the wide pair of 192 columns.
 // (Stores from registers, 32 bytes a thread and row, were tried: the 32
 // single-sector accesses of a warp instruction made the epilogue of a 128 x 256
-// tile 11000 cycles instead of 7000.)
+// tile 11000 cycles instead of 7000.  Sixteen warps of 32 columns on tiles of
+// 128 columns have 96 registers a thread and spill: 4096 x 4608 x 1152 int8 with
+// gelu_tanh and residual 25.0 -> 26.4 us.)
 template <int BN>
 constexpr bool kWide = BN <= 192;
 constexpr int kEpBox = 32 * 128;
@@ -912,9 +916,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    // The warp runs the loop converged and one elected thread issues: the loop
-    // itself (barrier tests, descriptors, commits) would otherwise take longer
-    // than the four MMAs of a K block of up to 192 columns.
+    // The warp runs the loop converged and one elected thread issues: issued
+    // from inside one lane's branch the loop itself (barrier tests, descriptors,
+    // commits) was in the MMAs' way where a tile has few K blocks (256 x 1024 x
+    // 1024 int8 6.2 -> 5.5 us, 16384 x 4096 x 8192 349 -> 335 us).
     int stage = 0;
     uint32_t phase = 0;
     int acc_iter = 0;

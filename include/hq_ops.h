@@ -71,8 +71,7 @@ typedef struct hq_epilogue {
  * or, in the weight-only Hadamard form, the output-side transform's result
  * plus bias.  Every description, code format and argument of hq_linear;
  * `epilogue` may be NULL (the results are then those of hq_linear, bit for bit).
- * N is a multiple of 16
- * and T < 2^31 - 256. */
+ * N is a multiple of 16, N <= 2^30 and T <= 2^31 - 256. */
 hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
                        const float* a_scale, const float* a_mean, const int8_t* w_codes,
                        const float* w_scale, const float* colsum, const float* bias_f32,
@@ -80,7 +79,7 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
                        hq_stream_t stream);
 
 /* A 16-bit linear layer: K input and N output channels, both multiples of 8;
- * K <= 2^20. */
+ * K <= 2^20, N <= 2^30. */
 typedef struct hq_dense_desc {
   int32_t K, N;
 } hq_dense_desc;
@@ -91,9 +90,9 @@ typedef struct hq_dense_desc {
  * Inputs:  X bf16 [T,K], W bf16 [N,K] (the nn.Linear orientation), bias bf16
  *          [N] or NULL; `epilogue` may be NULL (Y = bf16(z)).
  * Output:  Y bf16 [T,N]; it overlaps no input but the residual it may equal.
- * T >= 0 (T = 0 is a no-op), T < 2^31 - 256.  All pointers 16-byte aligned.
+ * T >= 0 (T = 0 is a no-op), T <= 2^31 - 256.  All pointers 16-byte aligned.
  * Results are deterministic: every sum over K is taken in an order that
- * depends on the sizes alone. */
+ * depends on the sizes and the device's SM count alone. */
 hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, const uint16_t* W,
                    const uint16_t* bias, const hq_epilogue* epilogue, uint16_t* Y,
                    hq_stream_t stream);
@@ -107,7 +106,8 @@ typedef struct hq_group_norm_desc {
   float eps;
 } hq_group_norm_desc;
 
-/* Bytes of device workspace hq_group_norm needs for B images of S pixels. */
+/* Bytes of device workspace hq_group_norm needs for B images of S pixels on the
+ * current device (0: nothing to do, or a description that the call refuses). */
 size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, int64_t S);
 
 /* hq_group_norm -- over every image b and group g, with the mean and the
@@ -116,11 +116,12 @@ size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, 
  * Inputs:  X bf16 [B,S,C]; gamma, beta bf16 [C] or NULL (1 and 0).
  * Output:  Y bf16 [B,S,C]; may be X itself, may not overlap it otherwise.
  * workspace: device, 16-byte aligned, >= hq_group_norm_workspace_bytes()
- *   bytes (NULL where that is 0); contents need not be initialised.
- * Statistics are held in fp32 as means and sums of squared deviations, merged
- * pairwise-exactly (no difference of large sums), in an order that depends on
- * the sizes alone.  B = 0 or S = 0 is a no-op.  X and Y 16-byte aligned, gamma
- * and beta 16-byte aligned. */
+ *   bytes; contents need not be initialised.
+ * Statistics are held in fp32 as means and sums of squared deviations around a
+ * value of the group (never a difference of large sums), in an order that
+ * depends on the sizes and the device's SM count alone.  A NaN or an infinity
+ * makes its image's group NaN and touches no other.  B = 0 or S = 0 is a no-op.
+ * B, S < 2^31.  X, Y, gamma and beta 16-byte aligned. */
 hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64_t B, int64_t S,
                         const uint16_t* gamma, const uint16_t* beta, uint16_t* Y, void* workspace,
                         size_t workspace_bytes, hq_stream_t stream);

@@ -135,8 +135,8 @@ def pack_i4(codes):
     return ((c[:, 0::2] & 15) | ((c[:, 1::2] & 15) << 4)).to(torch.uint8)
 
 
-def group_norm64(X, G, gamma, beta, eps, act):
-    """(exact, tol).  The statistics are sums of at most n_sum = 700 parts one
+def group_norm64(X, G, gamma, beta, eps, act, n_sum=700):
+    """(exact, tol).  The statistics are sums of at most n_sum parts one
     after the other (rows of a thread, threads, channels, chunks); with D the
     group's largest distance between values:
       mean off by <= n_sum u D;  variance, relative: n_sum u (1 + 4 D^2 / var),
@@ -148,7 +148,6 @@ def group_norm64(X, G, gamma, beta, eps, act):
     D = x.amax(dim=(1, 3), keepdim=True) - x.amin(dim=(1, 3), keepdim=True)
     rstd = 1 / torch.sqrt(var + eps)
     n = (x - mean) * rstd
-    n_sum = 700
     dn = n_sum * U * (D * rstd + n.abs() * 0.5 * (1 + 4 * D ** 2 / (var + eps))) + 8 * U * n.abs()
     dn = dn + 2 * U * x.abs() * rstd
     ga = (torch.ones(C, device=X.device) if gamma is None else gamma).double().view(G, -1)

@@ -554,3 +554,67 @@ def test_modulated_mlp(hq):
                     GELU_TANH)[0]
     yd = X.double() + gd.repeat_interleave(S, 0) * (hd @ W2.double().t() + b2.double())
     assert rel_frob(Y, yd) < 0.02
+
+
+# ------------------------------------------------- tensors past 2^31 elements
+def _windows(T, at, n=300):
+    """Row ranges: the first, those around `at` and the last."""
+    return [slice(0, n), slice(at - n // 2, at + n // 2), slice(T - n, T)]
+
+
+def test_dense_past_31_bits(hq):
+    g = _gen(41)
+    T, K, N = (1 << 20) + 5, 8, 2056
+    assert T * N > 2 ** 31
+    X, W = _bf(_randn(g, T, K)), _bf(_randn(g, N, K) * K ** -0.5)
+    G = _bf(_randn(g, -(-T // 1000), N))
+    Y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    wins = _windows(T, 2 ** 31 // N)
+    R = [Y[w].clone() for w in wins]
+    hq.hq_dense(hq.DenseDesc(K, N), X, W, None, hq.Epilogue(SILU, Y, G, 1000), Y)
+    assert hq.hq_check_device_error() == 0
+    for w, r in zip(wins, R):
+        z, ztol = dense64(X[w], W, None)
+        rows = torch.arange(w.start, w.stop, device="cuda") // 1000
+        y, tol = epilogue64(z, ztol, SILU, r, G[rows], 1)
+        check_rounded(Y[w], y, tol, f"rows {w}")
+
+
+def test_linear_ep_past_31_bits(hq):
+    g = _gen(42)
+    T, K, N = (1 << 20) + 5, 16, 2064
+    assert T * N > 2 ** 31
+    A, W = _codes(g, T, K, 4), _codes(g, N, K, 4)
+    sx = torch.rand(T, generator=g, device="cuda") + 0.5
+    sw = (torch.rand(N, generator=g, device="cuda") + 0.5) / 256
+    Y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    wins = _windows(T, 2 ** 31 // N)
+    R = [Y[w].clone() for w in wins]
+    desc = hq.LayerDesc(K, N, 16, a_bits=4, w_bits=4, centering=hq.HQ_CENTER_NONE)
+    hq.hq_linear_ep(desc, A, sx, None, W, sw, None, None, hq.Epilogue(GELU_TANH, Y), Y)
+    assert hq.hq_check_device_error() == 0
+    for w, r in zip(wins, R):
+        z, ztol = linear64(A[w], sx[w], None, W, sw, None, None)
+        y, tol = epilogue64(z, ztol, GELU_TANH, r)
+        check_rounded(Y[w], y, tol, f"rows {w}")
+
+
+@pytest.mark.parametrize("B,S,C,G", [(1, (1 << 25) + 3, 72, 8), (3, (1 << 23) + 1, 96, 8)])
+def test_group_norm_past_31_bits(hq, B, S, C, G):
+    assert B * S * C > 2 ** 31
+    g = _gen(43)
+    X = torch.empty(B, S, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    X[:, S // 2:] += 2                     # the halves differ: a part that is missed shows
+    ga, be = _bf(1 + 0.3 * _randn(g, C)), _bf(0.5 * _randn(g, C))
+    Y = hq.GroupNorm(C, G, ga, be, act=SILU)(X)
+    assert hq.hq_check_device_error() == 0
+    for b in range(B):
+        chunks = X[b].split(1 << 21)
+        n = S * (C // G)
+        mean = sum(c.double().view(-1, G, C // G).sum(dim=(0, 2)) for c in chunks) / n
+        m = mean.repeat_interleave(C // G)
+        var = sum(((c.double() - m) ** 2).view(-1, G, C // G).sum(dim=(0, 2)) for c in chunks) / n
+        rstd = (1 / torch.sqrt(var + 1e-5)).repeat_interleave(C // G)
+        for w in _windows(S, min(2 ** 31 // C, S // 2)):
+            z = (X[b, w].double() - m) * rstd * ga.double() + be.double()
+            assert rel_frob(Y[b, w], z / (1 + torch.exp(-z))) < ROUND_FROB

@@ -131,3 +131,12 @@ def test_block_refusals(hq):
         hq.PointwiseBlock(norm, Layer(), residual=True)
     with pytest.raises(ValueError, match="HadamardQuantLinear"):
         hq.PointwiseBlock(norm, Layer(), act=hq.HQ_ACT_SILU)
+
+
+def test_sizes_past_the_coordinates_are_refused(hq):
+    lib = hq.load_library()
+    d = hq.DenseDesc(8, 2 ** 30 + 8)
+    assert lib.hq_dense(ctypes.byref(d), FAKE, 1, 64 * FAR, None, None, FAR, None) == UNSUPPORTED
+    d = hq.LayerDesc(16, 2 ** 30 + 16, 16)
+    assert lib.hq_linear_ep(ctypes.byref(d), 1, FAKE, 2 * FAKE, None, 64 * FAR, 3 * FAR, None, None,
+                            None, 5 * FAR, None, None) == UNSUPPORTED
