@@ -960,7 +960,8 @@ class GroupNorm:
                     nb = hq_group_norm_workspace_bytes(self.desc, key[1],
                                                        n // (key[1] * self.desc.C))
                 self._ws_bytes[key] = nb
-            ws = X.new_empty(nb, dtype=rt.u8)
+            if nb:
+                ws = X.new_empty(nb, dtype=rt.u8)
         hq_group_norm(self.desc, X, self.gamma, self.beta, Y, ws)
         return Y
 

@@ -1878,7 +1878,7 @@ size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, 
   p.G = desc->groups;
   int vec;
   gn_plan(&p, &vec, sms_or_default());
-  return size_t(B) * size_t(p.P) * size_t(p.G) * sizeof(float2);
+  return gn_workspace(p);
 }
 
 hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64_t B, int64_t S,
@@ -1916,11 +1916,13 @@ hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64
   p.eps = desc->eps;
   int vec;
   gn_plan(&p, &vec, dev->sm_count);
-  const size_t need = size_t(B) * size_t(p.P) * size_t(p.G) * sizeof(float2);
-  if (workspace == nullptr || workspace_bytes < need) return HQ_ERR_INVALID_ARGUMENT;
-  if (!aligned16(workspace)) return HQ_ERR_MISALIGNED;
-  if (overlaps(workspace, need, X, bytes) || overlaps(workspace, need, Y, bytes))
-    return HQ_ERR_INVALID_ARGUMENT;
+  const size_t need = gn_workspace(p);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return HQ_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return HQ_ERR_MISALIGNED;
+    if (overlaps(workspace, need, X, bytes) || overlaps(workspace, need, Y, bytes))
+      return HQ_ERR_INVALID_ARGUMENT;
+  }
   p.part = static_cast<float2*>(workspace);
   return from_cuda(launch_group_norm(vec, p, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -309,6 +309,9 @@ struct GnParams {
   float eps;
   float2* part;           // [B][P][G] (mean, sum of squared deviations)
   // the rest is gn_plan's: chunks of rows_p rows (the last rows_last), P an image
+  // slices: 0, or the small form's: slices of gs groups an image, each of its
+  // P = 2^log_p chunks a CTA of one cluster
+  int slices, log_p;
   int cpg;                // channels per group
   int P, rows_p, rows_last;
   float n_full, n_last;   // values of a group in a chunk
@@ -325,8 +328,11 @@ struct GnParams {
 };
 
 // Fills in the plan of p (B, S, C and G set) and the channels per load (host
-// only).
+// only); gn_workspace: the bytes that the plan needs.
 void gn_plan(GnParams* p, int* vec, int sms);
+inline size_t gn_workspace(const GnParams& p) {
+  return p.slices ? 0 : size_t(p.B) * size_t(p.P) * size_t(p.G) * sizeof(float2);
+}
 cudaError_t launch_group_norm(int vec, const GnParams& p, cudaStream_t st);
 
 }  // namespace hq

@@ -3,7 +3,8 @@
 //   y = act((x - mean) / sqrt(var + eps) * gamma_c + beta_c)
 //
 // with mean and variance over the S pixels and C / G channels of an image's
-// group.  Two launches: gn_stats_kernel leaves (mean, M2 = sum of squared
+// group.  A small tensor is one launch, gn_small_kernel, in registers.  Others
+// are two: gn_stats_kernel leaves (mean, M2 = sum of squared
 // deviations) of every row chunk and group in the workspace; gn_apply_kernel,
 // launched as its programmatic dependent (it starts while the first drains,
 // loads its first rows, and waits), merges the chunks' statistics, normalizes
@@ -20,14 +21,12 @@
 // around the first of them.  Orders depend on sizes alone; equal values give
 // exactly their mean and M2 = 0.
 //
-// Why two passes of one CTA an SM: a group of a few thousand pixels does not fit
-// an SM, and keeping an image's groups resident over a cluster (X read once) was
-// tried first and took 59 us for 16 x 4096 x 320 and 184 us for 262144 x 128:
-// every unit of work paid a load, a cluster barrier and a store one after the
-// other.  Streaming takes 26.0 us (42 + 42 + 42 MB, the second read mostly from
+// Why two passes of one CTA an SM, where the tensor does not fit the registers:
+// keeping a few groups at a time resident over a cluster (X read once) was tried
+// first and took 59 us for 16 x 4096 x 320 and 184 us for 262144 x 128: every
+// unit of work paid a load, a cluster barrier and a store one after the other.  Streaming takes 26.0 us (42 + 42 + 42 MB, the second read mostly from
 // L2: 3.2 TB/s of X read once and Y written) and 38.0 us (67 MB in, 67 MB out:
-// 3.5 TB/s); one image of 4096 x 320 takes 8.3 us, five dependent trips to
-// memory and the launches.  The statistics pass runs near the memory's rate; the
+// 3.5 TB/s).  The statistics pass runs near the memory's rate; the
 // normalization is bound by issue slots and special functions (about 120
 // instructions for 8 channels with silu), and two CTAs an SM, or three or one
 // rows a batch, made it slower (28 to 30 us).
@@ -477,6 +476,93 @@ __global__ void __launch_bounds__(kGnThreads, 1) gn_apply_kernel(const GnParams 
   });
 }
 
+// The small form: an image's slice of whole groups is one cluster's, which
+// holds it in registers.  Each CTA takes a chunk of rows, sends its chunk's
+// statistics to every CTA of the cluster, merges all of them in the order of
+// the chunks, normalizes and stores.  One launch, X read once.
+constexpr int kSmallBytes = 128;  // of X that a thread can hold
+
+template <int VEC>
+__global__ void __launch_bounds__(kGnThreads, 1) gn_small_kernel(const GnParams p) {
+  extern __shared__ float2 sm[];
+  const int M = p.nv * VEC;  // channels of the slice, at most kGnThreads
+  float2* part = sm;                                // [VEC][kPartLd]
+  float2* sums = sm + VEC * kPartLd;                // [kGnThreads]
+  float2* mine = sums + kGnThreads;                 // [gs]
+  float2* all = mine + p.gs;                        // [P][gs]
+  float* coef = reinterpret_cast<float*>(all + (p.gs << p.log_p));  // [3][M]
+  if (p.log_p) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int chunk = int(blockIdx.x) & (p.P - 1);
+  const int unit = int(blockIdx.x) >> p.log_p;
+  const int b = unit / p.slices, c0 = (unit - b * p.slices) * M;
+  const bool last = chunk == p.P - 1;
+  const int rows = last ? p.rows_last : p.rows_p;
+  const int nv = p.nv, RP = p.RP;
+  const int rp = div_small(int(threadIdx.x), p.magic_nv), cv = int(threadIdx.x) - rp * nv;
+  const int q = last ? p.q_last : p.q_full, rem = rows - q * RP;
+  const int cnt = rp >= RP ? 0 : rp < rem ? q + 1 : q;
+  const int64_t base = (int64_t(b) * p.S + int64_t(chunk) * p.rows_p + rp) * p.C + c0 + cv * VEC;
+  const int step = RP * p.C;
+  typedef typename Vec<VEC>::T V;
+  constexpr int U = kSmallBytes / (2 * VEC);
+  V raw[U];
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+    if (j < cnt) raw[j] = *reinterpret_cast<const V*>(p.X + base + j * step);
+  float ga = 1.0f, be = 0.0f;
+  if (int(threadIdx.x) < M) {
+    ga = bf16_at(p.gamma, c0 + int(threadIdx.x), 1.0f);
+    be = bf16_at(p.beta, c0 + int(threadIdx.x), 0.0f);
+  }
+  if (cnt > 0) {
+    ThreadStats<VEC> ts;
+    ts.start(raw[0]);
+#pragma unroll
+    for (int j = 1; j < U; ++j)  // (the first value adds nothing around itself)
+      if (j < cnt) ts.add(raw[j]);
+    ts.finish(cnt, part);
+  }
+  __syncthreads();
+  block_group_stats<VEC>(p, part, sums, min(RP, rows), nv, p.cpg, p.gs,
+                         last ? p.inv_n_last : p.inv_n_full, rem, float(q), M, float(rows), 0.0f,
+                         p.log_p ? mine : all);
+  if (p.log_p) {
+    __syncthreads();
+    // every CTA of the cluster has started
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int i = threadIdx.x; i < p.gs << p.log_p; i += kGnThreads) {
+      const int g = i >> p.log_p;
+      const uint32_t to = mapa_shared(all + chunk * p.gs + g, uint32_t(i & (p.P - 1)));
+      st_shared_cluster_u32(to, __float_as_uint(mine[g].x));
+      st_shared_cluster_u32(to + 4, __float_as_uint(mine[g].y));
+    }
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (int(threadIdx.x) < M) {
+    const int c = int(threadIdx.x), g = div_small(c, p.magic_cpg);
+    Merge m{all[g].x, 0.0f, 0.0f};
+    for (int k = 0; k < p.P; ++k)
+      m.add(k == p.P - 1 ? p.n_last : p.n_full, all[k * p.gs + g]);
+    const float2 st = mean_rstd(m.finish(p.inv_n), p.inv_n, p.eps);
+    coef[c] = st.x;
+    coef[M + c] = st.y * ga;
+    coef[2 * M + c] = be;
+  }
+  __syncthreads();
+  if (cnt == 0) return;
+  with_act(p.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    Normalize<VEC> nz;
+    nz.load(coef, M, cv * VEC);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (j < cnt)
+        *reinterpret_cast<V*>(p.Y + base + j * step) = nz.template apply<ACT>(raw[j]);
+  });
+}
+
 // ---------------------------------------------------------------------- plan
 namespace {
 
@@ -499,12 +585,100 @@ int log2_floor(int v) {
 
 }  // namespace
 
+namespace {
+
+// Per-channel and per-group merging of a CTA's parts (block_group_stats), for
+// slices of p->gs groups = p->nv vectors.
+void plan_merge(GnParams* p, int vec) {
+  const int M = p->nv <= kGnThreads ? p->nv * vec : kGnThreads * vec;
+  const int gcpg = M / p->gs;
+  p->kk = M >= kGnThreads ? 1 : kGnThreads / M;
+  if (p->kk > p->RP) p->kk = p->RP;
+  p->magic_m = magic_of(M);
+  int lanes = 32;
+  while (lanes > 1 && (lanes * p->gs > kGnThreads || lanes >= 2 * gcpg)) lanes >>= 1;
+  p->lanes = lanes;
+  p->log_lanes = log2_floor(lanes);
+}
+
+// The chunks of `rows` rows and what follows from them.
+void plan_chunks(GnParams* p, int64_t rows) {
+  p->rows_p = int(rows);
+  p->P = int((p->S + rows - 1) / rows);
+  p->rows_last = int(p->S - (p->P - 1) * rows);
+  p->n_full = float(rows) * float(p->cpg);
+  p->n_last = float(p->rows_last) * float(p->cpg);
+  p->inv_n = float(1.0 / (double(p->S) * p->cpg));
+  p->inv_n_full = float(1.0 / (double(rows) * p->cpg));
+  p->inv_n_last = float(1.0 / (double(p->rows_last) * p->cpg));
+}
+
+// The small form, where a cluster's registers hold an image's slice and all
+// clusters run at once, one CTA an SM (clusters of four and eight leave some SMs
+// without one).  Modelled time beyond its fixed 4.6 us: what a row a thread
+// costs, the cluster's exchange, and slices of less than two sectors.  Fitted to
+// sweeps of 1 to 16384 pixels of 64 to 1280 channels in 1 to 140 images (within
+// 0.5 us, the choice within 0.3 us of the best).  The two launches take 5 us at
+// least and 8 to 9 where this form takes 4.8 to 7.2 (1 x 64 x 1280 8.3 -> 4.8, 4 x
+// 1024 x 320 8.0 -> 6.2, 1 x 4096 x 320 8.3 -> 6.9, 30 x 256 x 320 14.8 -> 6.5).
+// Narrower vectors lose the gain (3 x 5041 x 182: 8.8 us by two launches, 12.3
+// so) and are left to the two launches.
+bool gn_small_plan(GnParams* p, int* vec, int sms) {
+  if (p->B > sms) return false;
+  for (int v : {8, 4}) {
+    if (p->C % v != 0) continue;
+    const int unit = v / gcd(p->cpg, v);
+    double best = 1e30;
+    for (int gs = unit; gs <= p->G && gs * p->cpg <= kGnThreads; gs += unit) {
+      if (p->G % gs != 0) continue;
+      const int RP = kGnThreads / (gs * p->cpg / v);
+      // a slice's part of a row: the whole row, at least a sector of 32 bytes, and
+      // better two
+      const int segment = gs == p->G ? 64 : 2 * gs * p->cpg;
+      if (segment < 32) continue;
+      for (int lp = 0; lp <= 3; ++lp) {
+        if (lp > 0 && p->S < (64 << lp)) break;
+        const int64_t rows = (p->S + (1 << lp) - 1) >> lp;
+        const int64_t each = (rows + RP - 1) / RP;  // a thread
+        const int64_t grid = (p->B * (p->G / gs)) << lp;
+        const int64_t at_once = lp == 3 ? sms * 3 / 4 : lp == 2 ? sms * 7 / 8 : sms;
+        if (each > kSmallBytes / (2 * v) || grid > at_once || (segment < 64 && each > 4)) continue;
+        const double cost = (each <= 3 ? 0.36 * double(each) : 0.42 + 0.22 * double(each)) +
+                            (lp > 0 ? 0.5 + 0.05 * lp : 0.0) + (segment < 64 ? 0.8 : 0.0);
+        if (cost < best) {
+          best = cost;
+          p->gs = gs;
+          p->log_p = lp;
+        }
+      }
+    }
+    if (best < 1e30) {
+      *vec = v;
+      p->slices = p->G / p->gs;
+      plan_chunks(p, (p->S + (1 << p->log_p) - 1) >> p->log_p);
+      p->nv = p->gs * p->cpg / v;
+      p->RP = kGnThreads / p->nv;
+      p->q_full = p->rows_p / p->RP;
+      p->q_last = p->rows_last / p->RP;
+      p->magic_nv = magic_of(p->nv);
+      p->magic_cpg = magic_of(p->cpg);
+      plan_merge(p, v);
+      return true;
+    }
+  }
+  return false;
+}
+
+}  // namespace
+
 // Row chunks and vector width (see GnParams): one CTA an SM over the whole
 // batch, two where one leaves more than a tenth of the SMs idle; chunks of less
 // than 2^30 elements.
 void gn_plan(GnParams* p, int* vec, int sms) {
   const int C = p->C, G = p->G, cpg = C / G;
   p->cpg = cpg;
+  p->slices = 0;
+  if (gn_small_plan(p, vec, sms)) return;
   // the widest vectors whose slices of whole groups fit a CTA's threads
   for (int v : {8, 4, 2, 1}) {
     if (C % v != 0) continue;
@@ -524,29 +698,14 @@ void gn_plan(GnParams* p, int* vec, int sms) {
   const int64_t least = (p->S * C >> 30) + 1;
   want = want > p->S ? p->S : want < least ? least : want;
   const int64_t rows = (p->S + want - 1) / want;
-  p->rows_p = int(rows);
-  p->P = int((p->S + rows - 1) / rows);
-  p->rows_last = int(p->S - (p->P - 1) * rows);
-  p->n_full = float(rows) * float(cpg);
-  p->n_last = float(p->rows_last) * float(cpg);
-  p->inv_n = float(1.0 / (double(p->S) * cpg));
+  plan_chunks(p, rows);
   // statistics
-  p->inv_n_full = float(1.0 / (double(rows) * cpg));
-  p->inv_n_last = float(1.0 / (double(p->rows_last) * cpg));
   p->nv = p->gs * cpg / *vec;
   p->RP = p->nv <= kGnThreads ? kGnThreads / p->nv : 1;
   p->magic_nv = magic_of(p->nv);
   p->q_full = p->rows_p / p->RP;
   p->q_last = p->rows_last / p->RP;
-  const int M = p->nv <= kGnThreads ? p->nv * *vec : kGnThreads * *vec;
-  const int gcpg = M / p->gs;
-  p->kk = M >= kGnThreads ? 1 : kGnThreads / M;
-  if (p->kk > p->RP) p->kk = p->RP;
-  p->magic_m = magic_of(M);
-  int lanes = 32;
-  while (lanes > 1 && (lanes * p->gs > kGnThreads || lanes >= 2 * gcpg)) lanes >>= 1;
-  p->lanes = lanes;
-  p->log_lanes = log2_floor(lanes);
+  plan_merge(p, *vec);
   // normalization
   const int CV = C / *vec;
   p->nva = CV < kGnThreads ? CV : kGnThreads;
@@ -582,7 +741,32 @@ struct AttrOnce {
 };
 
 template <int VEC>
+cudaError_t launch_small(const GnParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.B * p.slices) << p.log_p);
+  cfg.blockDim = dim3(kGnThreads);
+  cfg.dynamicSmemBytes = sizeof(float2) * (size_t(kPartLd) * VEC + kGnThreads + p.gs +
+                                           (size_t(p.gs) << p.log_p)) +
+                         sizeof(float) * 3 * size_t(p.nv * VEC);
+  cfg.stream = st;
+  static AttrOnce once;
+  const cudaError_t e = once.set((const void*)gn_small_kernel<VEC>, 80 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = 1u << p.log_p;
+  a[0].val.clusterDim.y = 1;
+  a[0].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = p.log_p ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gn_small_kernel<VEC>, p);
+}
+
+template <int VEC>
 cudaError_t launch_vec(const GnParams& p, cudaStream_t st) {
+  if constexpr (VEC >= 4) {
+    if (p.slices) return launch_small<VEC>(p, st);
+  }
   const int M = p.nv <= kGnThreads ? p.nv * VEC : kGnThreads * VEC;
   const size_t smem_s =
       sizeof(float2) * (size_t(kPartLd) * VEC + size_t(M > kGnThreads ? M : kGnThreads));

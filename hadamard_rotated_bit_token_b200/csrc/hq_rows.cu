@@ -6,12 +6,12 @@
 // 128 tokens on the tensor cores would move no more bytes but pays for tensor
 // memory, tensor maps and a pipeline before the first byte arrives, and leaves
 // most SMs without a tile (4 x 1152 x 6912 in bf16, 16 MB of B: 10.7 us by
-// tiles of 128 x 192, 4.8 us by this kernel, B coming from L2;
-// 1 x 256 x 1152 takes 2.2 us, nearly all of it launch and one trip to memory).  Here B's rows go straight from global
-// memory into registers: a warp takes R rows of B and a share of K, each lane 16
-// bytes of each row a step, multiplied by the same 16 bytes of every token (from
-// L1 after the first row); WK warps share the K of the same rows, so that narrow
-// layers still fill the GPU with loads in flight.
+// tiles of 128 x 192, 4.8 us by this kernel, B coming from L2; 2 x 256 x 1152
+// takes 2.3 us, nearly all of it launch and one trip to memory).  Here B's rows
+// go straight from global memory into registers: a warp takes R rows of B and a
+// share of K, each lane 16 bytes of each row a step, multiplied by the same 16
+// bytes of every token (from L1 after the first row); WK warps share the K of
+// the same rows, so that narrow layers still fill the GPU with loads in flight.
 //
 // Sums: bf16 products are exact in fp32 and summed in fp32 (a lane's steps in
 // order, then lanes, then warps: a tree that depends on the sizes alone); int8

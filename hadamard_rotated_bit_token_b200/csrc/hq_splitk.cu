@@ -74,10 +74,6 @@ struct SkCfg {
   static_assert(16 * STAGES + 32 <= CTL_BYTES, "barrier block");
 };
 
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // sum + the partial sums v, per element
 template <int KIND>
 __device__ __forceinline__ void add_parts(uint4& sum, const uint4& v) {
@@ -300,8 +296,8 @@ __global__ void __launch_bounds__(kSkThreads, 2)
         for (int i = 0; i < 32; ++i) {
           const int t = c + i;
           if (t < NT && t0 + t < p.T)
-            st_cluster_u32(mapa_shared(dst + (t & (own - 1)) * kSkRows, uint32_t(t >> log_own)),
-                           r[i]);
+            st_shared_cluster_u32(
+                mapa_shared(dst + (t & (own - 1)) * kSkRows, uint32_t(t >> log_own)), r[i]);
         }
       }
     } else if (!got) {

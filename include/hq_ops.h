@@ -107,7 +107,8 @@ typedef struct hq_group_norm_desc {
 } hq_group_norm_desc;
 
 /* Bytes of device workspace hq_group_norm needs for B images of S pixels on the
- * current device (0: nothing to do, or a description that the call refuses). */
+ * current device: 0 where it needs none (small tensors), where there is nothing
+ * to do, and for a description that the call refuses. */
 size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, int64_t S);
 
 /* hq_group_norm -- over every image b and group g, with the mean and the
@@ -116,7 +117,7 @@ size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, 
  * Inputs:  X bf16 [B,S,C]; gamma, beta bf16 [C] or NULL (1 and 0).
  * Output:  Y bf16 [B,S,C]; may be X itself, may not overlap it otherwise.
  * workspace: device, 16-byte aligned, >= hq_group_norm_workspace_bytes()
- *   bytes; contents need not be initialised.
+ *   bytes (NULL where that is 0); contents need not be initialised.
  * Statistics are held in fp32 as means and sums of squared deviations around a
  * value of the group (never a difference of large sums), in an order that
  * depends on the sizes and the device's SM count alone.  A NaN or an infinity

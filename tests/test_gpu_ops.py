@@ -618,3 +618,31 @@ def test_group_norm_past_31_bits(hq, B, S, C, G):
         for w in _windows(S, min(2 ** 31 // C, S // 2)):
             z = (X[b, w].double() - m) * rstd * ga.double() + be.double()
             assert rel_frob(Y[b, w], z / (1 + torch.exp(-z))) < ROUND_FROB
+
+
+# small tensors: slices of whole groups held by clusters of one to eight blocks,
+# the last chunk of rows shorter, sizes on both sides of what they can hold
+@pytest.mark.parametrize("B,S,C,G", [
+    (1, 4095, 320, 32), (1, 127, 64, 8), (1, 128, 64, 8), (1, 257, 1280, 32), (4, 1023, 320, 32),
+    (2, 4096, 320, 32), (30, 255, 320, 32), (148, 3, 16, 2), (149, 3, 16, 2), (1, 4096, 36, 9),
+    (1, 4097, 640, 32), (2, 1000, 100, 5), (1, 513, 512, 512), (7, 65, 24, 1), (1, 3277, 320, 32),
+    (1, 6553, 320, 32), (1, 2049, 1280, 32)])
+def test_group_norm_small(hq, B, S, C, G):
+    g = _gen(B + S + C + G)
+    X = _bf(_randn(g, B, S, C) * torch.exp(0.5 * _randn(g, 1, 1, C)) + _randn(g, B, 1, C))
+    ga, be = _bf(1 + 0.3 * _randn(g, C)), _bf(0.5 * _randn(g, C))
+    norm = hq.GroupNorm(C, G, ga, be, act=SILU)
+    Y = norm(X)
+    y, tol = group_norm64(X, G, ga, be, 1e-5, SILU)
+    check_rounded(Y, y, tol, f"group norm {B}x{S}x{C} G{G}")
+    assert rel_frob(Y, y) < ROUND_FROB
+    Z = X.clone()
+    norm(Z, Z)                              # in place
+    assert torch.equal(Z, Y)
+    poisoned = X.clone()                    # an infinity stays in its image and group
+    poisoned[0, S // 2, 0] = float("inf")
+    P = norm(poisoned)
+    n = C // G
+    assert bool(P[0, :, :n].isnan().all())
+    assert torch.equal(P[0, :, n:], Y[0, :, n:]) and torch.equal(P[1:], Y[1:])
+    assert hq.hq_check_device_error() == 0
