@@ -115,7 +115,7 @@ PROFILES = {("gemm", 2): "gemm_i8_cfg2_pixart_qkv.md", ("quant", 2): "quant_seg_
             ("gemm", 5): "gemm_i8_pair_cfg5_large_dit.md",
             ("quant", 5): "quant_wrow_cfg5_large_dit.md",
             ("gw_gemm", 5): "gw_gemm_cfg5_large_dit.md", ("gw_act", 5): "gw_act_cfg5_large_dit.md"}
-KERNEL_SOURCES = {"gemm": ("hq_gemm.cu", "hq_device.cuh", "hq_kernels.h"),
+KERNEL_SOURCES = {"gemm": ("hq_gemm.cu", "hq_gemm_tile.cuh", "hq_device.cuh", "hq_kernels.h"),
                   "quant": ("hq_quant_act.cu", "hq_quant_common.cuh", "hq_device.cuh",
                             "hq_kernels.h"),
                   "gw_gemm": ("hq_gw.cu", "hq_quant_common.cuh", "hq_device.cuh", "hq_kernels.h"),
