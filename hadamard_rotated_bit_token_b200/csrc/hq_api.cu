@@ -644,9 +644,10 @@ hq_status encode_out_bf16(CUtensorMap* m, const void* base, int64_t rows, int N)
 
 // GEMM kernel choice.  Both kernels are persistent with one CTA per SM, so a
 // launch takes about (tile rounds) x (time of one tile).  Measured on B200:
-// one 128 x n x 32 i8 MMA takes about 126 + n/16 cycles for n <= 256 --
-// nearly flat in n, so wide tiles win -- and the single-CTA main loop runs
-// about 15% behind that rate (operand loads).  The epilogue's traffic through
+// an MMA of 128 x n x 32 in the main loop goes as 126 + n/16 cycles for n <= 256
+// -- nearly flat in n, so wide tiles win (alone, issued by a converged warp, it
+// takes 64 at n = 128 and 128 at 256; the operands' passes through shared memory
+// level it) -- and the single-CTA main loop runs about 15% behind that rate.  The epilogue's traffic through
 // shared memory costs roughly 2000 cycles per 32-column chunk of each
 // epilogue warp (fitted to tile-width sweeps of several layer shapes).  The CTA pair halves the B bytes per
 // MMA but its 256 x 256 tiles carry twice the epilogue per CTA; it pays off
