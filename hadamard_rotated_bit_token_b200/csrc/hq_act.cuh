@@ -9,9 +9,10 @@
 // (hq_linear_ep 8192 x 1152 -> 4608 int4 with gelu: 60.6 -> 55.5 us; group norm
 // with silu over 16 images of 4096 x 320: 31.9 -> 31.4 us; d1 d2 adds two
 // roundings of 2^-24.  Newton steps on the FMA pipe instead of the reciprocal
-// made that 26.1 -> 28.4 us: issue slots are as scarce).  The product must not overflow, so z enters no lower
-// than where t reaches 63.5; there |z sigmoid(u)| is below 4e-18, and any z
-// below returns that or 0 (its value lies between the two).
+// made that 26.1 -> 28.4 us: issue slots are as scarce).  The product must not
+// overflow, so z enters no lower than where t reaches 63.5; there |z sigmoid(u)|
+// is below 4e-18, and any z below returns that or 0 (its value lies between the
+// two).
 //   silu       u = z                                                z >= -44
 //   gelu_tanh  0.5 (1 + tanh v) = sigmoid(2 v), so
 //              u = 2 sqrt(2/pi) (z + 0.044715 z^3)                   z >= -7.6
