@@ -24,12 +24,13 @@
 // Why two passes of one CTA an SM, where the tensor does not fit the registers:
 // keeping a few groups at a time resident over a cluster (X read once) was tried
 // first and took 59 us for 16 x 4096 x 320 and 184 us for 262144 x 128: every
-// unit of work paid a load, a cluster barrier and a store one after the other.  Streaming takes 26.0 us (42 + 42 + 42 MB, the second read mostly from
-// L2: 3.2 TB/s of X read once and Y written) and 38.0 us (67 MB in, 67 MB out:
-// 3.5 TB/s).  The statistics pass runs near the memory's rate; the
-// normalization is bound by issue slots and special functions (about 120
-// instructions for 8 channels with silu), and two CTAs an SM, or three or one
-// rows a batch, made it slower (28 to 30 us).
+// unit of work paid a load, a cluster barrier and a store one after the other.
+// Streaming takes 26.0 us (42 MB read, read again mostly from L2, 42 MB written:
+// 3.2 TB/s of X read once and Y written) and 38.0 us (67 MB in, 67 MB out: 3.5
+// TB/s).  The statistics pass runs near the memory's rate; the normalization is
+// bound by issue slots and special functions (about 120 instructions for 8
+// channels with silu), and two CTAs an SM, or one, two or three rows a batch,
+// made it slower (28 to 30 us).
 #include <cuda_bf16.h>
 
 #include <atomic>
