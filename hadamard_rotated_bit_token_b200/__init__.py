@@ -536,8 +536,10 @@ def _epilogue_ref(rt, ep, T, N, dev):
     """By-reference argument of an Epilogue (or None) for a [T, N] output."""
     if ep is None:
         return None
-    if ep.residual is not None:
-        ep._residual = _tensor(ep.residual, "residual", rt.bf16, (T, N), dev)
+    # both addresses anew at every call: the tensors may have been exchanged or
+    # taken away since the last one
+    ep._residual = _tensor(ep.residual, "residual", rt.bf16, (T, N), dev)
+    ep._gate = None
     if ep.gate is not None:
         if ep.gate_rows < 1:
             raise ValueError("a gate needs gate_rows >= 1 (rows of Y per row of the gate)")

@@ -140,3 +140,39 @@ def test_sizes_past_the_coordinates_are_refused(hq):
     d = hq.LayerDesc(16, 2 ** 30 + 16, 16)
     assert lib.hq_linear_ep(ctypes.byref(d), 1, FAKE, 2 * FAKE, None, 64 * FAR, 3 * FAR, None, None,
                             None, 5 * FAR, None, None) == UNSUPPORTED
+
+
+class _OnDevice:
+    """A stand-in for a CUDA tensor: what the binding asks of one, no memory."""
+
+    def __init__(self, address, shape, dtype):
+        self._address, self.shape, self.dtype, self.is_cuda = address, shape, dtype, True
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self._address
+
+
+def test_a_reused_epilogue_forgets_tensors_taken_away(hq):
+    """An Epilogue whose residual or gate is set to None after a call passes no
+    address of the old one on, and one that is exchanged passes the new one."""
+    torch = pytest.importorskip("torch")
+    bf16 = torch.bfloat16
+    rt = type("Runtime", (), {"bf16": bf16})
+    ep = hq.Epilogue(hq.HQ_ACT_SILU, _OnDevice(FAKE, (4, 64), bf16), _OnDevice(FAR, (2, 64), bf16), 2)
+    hq._epilogue_ref(rt, ep, 4, 64, 0)
+    assert (ep._residual, ep._gate) == (FAKE, FAR)
+    ep.residual = None
+    hq._epilogue_ref(rt, ep, 4, 64, 0)
+    assert (ep._residual, ep._gate) == (None, FAR)
+    ep.gate = _OnDevice(2 * FAR, (2, 64), bf16)
+    hq._epilogue_ref(rt, ep, 4, 64, 0)
+    assert (ep._residual, ep._gate) == (None, 2 * FAR)
+    ep.gate = None
+    hq._epilogue_ref(rt, ep, 4, 64, 0)
+    assert (ep._residual, ep._gate) == (None, None)
