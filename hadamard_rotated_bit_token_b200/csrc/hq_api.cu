@@ -49,6 +49,10 @@ int g_fault = 0;
 int g_gemm_variant = 0;  // HQ_GEMM_AUTO
 
 unsigned long long wait_ns() { return g_wait_ns ? g_wait_ns : 2000000000ull; }
+int injected_fault() {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  return g_fault;
+}
 
 hq_status device_state(DeviceState** out) {
   int dev = 0;
@@ -871,6 +875,7 @@ hq_status run_splitk(const DeviceState* dev, const SplitKPlan& pl, bool bf16, co
   p->num_n_tiles = (N + 127) / 128;
   p->err = dev->err;
   p->wait_ns = wait_ns();
+  p->withhold = injected_fault() == HQ_FAULT_SPLITK_WITHHOLD_STAGE;
   return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, st));
 }
 
@@ -1480,7 +1485,7 @@ hq_status hq_debug_tmap_cache(uint64_t* hits, uint64_t* misses) {
 }
 
 hq_status hq_debug_inject_fault(int kind) {
-  if (kind != HQ_FAULT_NONE && kind != HQ_FAULT_QUANT_WITHHOLD_ROW) return HQ_ERR_INVALID_ARGUMENT;
+  if (kind < HQ_FAULT_NONE || kind > HQ_FAULT_SPLITK_WITHHOLD_STAGE) return HQ_ERR_INVALID_ARGUMENT;
   std::lock_guard<std::mutex> lock(g_mutex);
   g_fault = kind;
   return HQ_OK;

@@ -181,6 +181,7 @@ struct SplitKParams {
   int N;
   int log_split, k_blocks, num_n_tiles;
   int stages, log_nt;        // (launch_splitk)
+  int withhold;              // test hook: 1 leaves each CTA's first stage unloaded
   // integer codes
   const float* a_scale;      // [T] or [1]
   int a_scale_per_row;

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kSkThreads, 2)
   uint64_t* tfull = empty + stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued = failed + 1;  // stages the producer has loaded
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{p.err, p.wait_ns};
@@ -205,19 +206,18 @@ __global__ void __launch_bounds__(kSkThreads, 2)
           *failed = 1;
           break;
         }
-        const int x = (kb0 + i) * 128;
-        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
-        tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, x, n0, &full[stage]);
-        tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, x, t0, &full[stage]);
+        if (!p.withhold || i > 0) {  // (withhold: the test hook's stage that never comes)
+          const int x = (kb0 + i) * 128;
+          mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+          tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, x, n0, &full[stage]);
+          tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, x, t0, &full[stage]);
+        }
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      // after a give-up the copies in flight land before the CTA can exit
-      if (i < nkb)
-        for (int j = i > stages ? i - stages : 0; j < i; ++j)
-          (void)mbar_wait(&full[j % stages], uint32_t(j / stages) & 1u, wc);
+      *issued = i;
     }
   } else {
     if (warp == 1) {
@@ -314,6 +314,14 @@ __global__ void __launch_bounds__(kSkThreads, 2)
   __syncthreads();
   cluster_sync();  // every CTA's partial sums are with their owners
 
+  // After a give-up, whichever wait it was, the copies in flight land and the
+  // MMAs issued complete before the CTA can exit.
+  if (*failed && threadIdx.x == 0) {
+    const int i = *issued;
+    for (int j = i > stages ? i - stages : 0; j < i; ++j)
+      (void)mbar_wait(&full[j % stages], uint32_t(j / stages) & 1u, wc);
+    (void)mbar_wait(tfull, 0, wc);
+  }
   if (!*failed && n < p.N) {
     const uint4* src = reinterpret_cast<const uint4*>(recv) + lane;
     for (int i = warp; i < own && tb + i < p.T; i += 2 * kWarps) {

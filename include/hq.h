@@ -303,8 +303,13 @@ hq_status hq_debug_set_gemm_variant(int variant);
  *       wait for it expires; otherwise the statistics of the first row of
  *       the first tile are never released.  The kernel records
  *       HQ_ERR_TIMEOUT, waits for the copies it did issue and exits.
+ *   HQ_FAULT_SPLITK_WITHHOLD_STAGE (2)   in each CTA of the next products with
+ *       an epilogue that split K over a cluster (hq_ops.h), the copy of the
+ *       first operand stage is never issued, so the tensor cores' bounded wait
+ *       for it expires.  The kernel records HQ_ERR_TIMEOUT, waits for the
+ *       copies it did issue and exits.
  * Host state, applies to launches issued after the call. */
-enum { HQ_FAULT_NONE = 0, HQ_FAULT_QUANT_WITHHOLD_ROW = 1 };
+enum { HQ_FAULT_NONE = 0, HQ_FAULT_QUANT_WITHHOLD_ROW = 1, HQ_FAULT_SPLITK_WITHHOLD_STAGE = 2 };
 hq_status hq_debug_inject_fault(int kind);
 
 /* Test hook, host only (no device call, usable without a GPU): the launch

@@ -176,3 +176,10 @@ def test_a_reused_epilogue_forgets_tensors_taken_away(hq):
     ep.gate = None
     hq._epilogue_ref(rt, ep, 4, 64, 0)
     assert (ep._residual, ep._gate) == (None, None)
+
+
+def test_known_faults_only(hq):
+    lib = hq.load_library()
+    assert lib.hq_debug_inject_fault(hq.HQ_FAULT_SPLITK_WITHHOLD_STAGE) == OK
+    assert lib.hq_debug_inject_fault(hq.HQ_FAULT_NONE) == OK
+    assert lib.hq_debug_inject_fault(-1) == INVALID and lib.hq_debug_inject_fault(100) == INVALID
