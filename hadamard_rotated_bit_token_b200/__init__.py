@@ -43,6 +43,7 @@ __all__ = [
     "HQ_CENTER_NONE", "HQ_CENTER_TOKEN_MEAN", "HQ_CENTER_TOKEN_MEAN_PRE", "HQ_CODES_I8",
     "HQ_CODES_I4_PACKED",
     "HQ_FAULT_NONE", "HQ_FAULT_QUANT_WITHHOLD_ROW", "HQ_FAULT_SPLITK_WITHHOLD_STAGE",
+    "HQ_FAULT_TILE_WITHHOLD_STAGE", "HQ_FAULT_TILE_WITHHOLD_RESIDUAL",
     "STATUS_NAMES",
     "hq_version", "hq_status_string", "hq_calib_act_absmax", "hq_prepare_weights",
     "hq_quantize_act_workspace_bytes", "hq_quantize_act", "hq_linear", "hq_forward_host",
@@ -64,6 +65,7 @@ HQ_PER_TOKEN, HQ_PER_TENSOR_DYNAMIC, HQ_PER_TENSOR_STATIC = 0, 1, 2
 HQ_CENTER_NONE, HQ_CENTER_TOKEN_MEAN, HQ_CENTER_TOKEN_MEAN_PRE = 0, 1, 2
 HQ_CODES_I8, HQ_CODES_I4_PACKED = 0, 1
 HQ_FAULT_NONE, HQ_FAULT_QUANT_WITHHOLD_ROW, HQ_FAULT_SPLITK_WITHHOLD_STAGE = 0, 1, 2
+HQ_FAULT_TILE_WITHHOLD_STAGE, HQ_FAULT_TILE_WITHHOLD_RESIDUAL = 3, 4
 HQ_GEMM_AUTO, HQ_GEMM_SINGLE_CTA, HQ_GEMM_CTA_PAIR = 0, 1, 2
 HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "HQ_OK", 1: "HQ_ERR_INVALID_ARGUMENT", 2: "HQ_ERR_UNSUPPORTED",

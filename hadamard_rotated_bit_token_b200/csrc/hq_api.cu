@@ -833,6 +833,10 @@ hq_status set_epilogue(GemmEpParams* p, const hq_epilogue* ep, const uint16_t* Y
   hq_status s = bn == 256 ? encode_out_bf16(map_y, Y, T, N) : encode_box64_bf16(map_y, Y, T, N);
   if (s != HQ_OK) return s;
   *map_r = *map_y;
+  const int fault = injected_fault();
+  p->withhold = fault == HQ_FAULT_TILE_WITHHOLD_STAGE      ? kWithholdStage
+                : fault == HQ_FAULT_TILE_WITHHOLD_RESIDUAL ? kWithholdResidual
+                                                           : 0;
   return bn != 256 && p->residual != nullptr && p->residual != Y
              ? encode_box64_bf16(map_r, p->residual, T, N)
              : HQ_OK;
@@ -1485,7 +1489,7 @@ hq_status hq_debug_tmap_cache(uint64_t* hits, uint64_t* misses) {
 }
 
 hq_status hq_debug_inject_fault(int kind) {
-  if (kind < HQ_FAULT_NONE || kind > HQ_FAULT_SPLITK_WITHHOLD_STAGE) return HQ_ERR_INVALID_ARGUMENT;
+  if (kind < HQ_FAULT_NONE || kind > HQ_FAULT_TILE_WITHHOLD_RESIDUAL) return HQ_ERR_INVALID_ARGUMENT;
   std::lock_guard<std::mutex> lock(g_mutex);
   g_fault = kind;
   return HQ_OK;

@@ -511,7 +511,9 @@ struct ResStream {
 
 // Lane 0: asks for R's box at (row0, col0), if it lies inside R.
 __device__ __forceinline__ void res_load(const GemmEpParams& p, ResStream& s, int row0, int col0) {
-  if (row0 < p.T && col0 < p.N) {
+  if (p.withhold == kWithholdResidual && s.issued == 0) {
+    // (the test hook's box that never comes)
+  } else if (row0 < p.T && col0 < p.N) {
     mbar_arrive_expect_tx(s.bar, kEpBox);
     tma_load_2d(s.box, s.tmR, col0, row0, s.bar);
   } else {
@@ -573,8 +575,8 @@ __device__ __forceinline__ bool epi_tile_ep(const GemmEpParams& p, const CUtenso
   // the box: R's has arrived, or the previous tile's store has read it
   if (has_res) {
     const bool got = mbar_wait(s.bar, s.used & 1u, wc);
+    if (!__all_sync(0xffffffffu, got)) return false;  // (not used: the caller waits again)
     ++s.used;
-    if (!__all_sync(0xffffffffu, got)) return false;
   } else {
     if (lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
@@ -752,6 +754,25 @@ __device__ __forceinline__ const uint16_t* gate_row_of(const GemmEpParams& p, in
 
 }  // namespace
 
+namespace {
+
+// Whether the test hook keeps the producer from loading stage `issued`.
+template <bool EP>
+__device__ __forceinline__ bool withheld(const GemmArgs<EP>& p, int issued) {
+  if constexpr (EP)
+    return p.withhold == kWithholdStage && issued == 0;
+  else
+    return false;
+}
+
+// The copies into the last two parameter slots, of `n` in all, have landed.
+__device__ __forceinline__ void wait_param_copies(uint64_t* pfull, uint32_t n, const WaitCtl& wc) {
+  for (uint32_t j = n > 2 ? n - 2 : 0; j < n; ++j)
+    (void)mbar_wait(&pfull[j & 1u], (j >> 1) & 1u, wc);
+}
+
+}  // namespace
+
 // ------------------------------------------------------- single-CTA kernel
 template <int KIND, int BN, bool PK, bool EP>
 struct GemmCfg {
@@ -788,7 +809,7 @@ struct GemmCfg {
   static_assert(B_BYTES % 1024 == 0, "stage bases must stay 1024-byte aligned");
   static_assert(STAGES >= 2, "shared / tensor memory budget");
   static_assert(!PK || 2 * BN + 32 * STAGES <= 512, "tensor memory budget");
-  static_assert(8 * NBAR_STAGE * STAGES + 80 + RES_BAR_BYTES <= CTL_BYTES, "barrier block");
+  static_assert(8 * NBAR_STAGE * STAGES + 88 + RES_BAR_BYTES <= CTL_BYTES, "barrier block");
   static_assert(KIND == kI8 || !PK, "packed codes are integers");
   static_assert(SMEM <= size_t(kSmemLimit), "shared memory budget");
 };
@@ -818,6 +839,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
   uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (wide epilogue)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (C::WIDE ? C::EPW : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* issued_by = tmem_slot + 2;  // [2]: stages and parameter slots loaded
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -885,13 +907,15 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
-          if constexpr (PK)  // K bytes of packed A per stage: BK / 2 (a multiple of 16)
-            tma_load_2d(sP + size_t(stage) * C::P_BYTES, tmA, kb * (BK / 2), m_idx * BM,
-                        &full[stage]);
-          else
-            tma_load_2d(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, m_idx * BM, &full[stage]);
-          tma_load_2d(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, n_idx * BN, &full[stage]);
+          if (!withheld<EP>(p, issued)) {
+            mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
+            if constexpr (PK)  // K bytes of packed A per stage: BK / 2 (a multiple of 16)
+              tma_load_2d(sP + size_t(stage) * C::P_BYTES, tmA, kb * (BK / 2), m_idx * BM,
+                          &full[stage]);
+            else
+              tma_load_2d(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, m_idx * BM, &full[stage]);
+            tma_load_2d(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, n_idx * BN, &full[stage]);
+          }
           ++issued;
           if (++stage == C::STAGES) {
             stage = 0;
@@ -899,20 +923,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
           }
         }
       }
-      if (!ok) {
-        // let the copies still in flight land before the CTA can exit
-        int s = stage;
-        uint32_t ph = phase;
-        for (int i = 0; i < C::STAGES && i < issued; ++i) {
-          if (--s < 0) {
-            s = C::STAGES - 1;
-            ph ^= 1u;
-          }
-          (void)mbar_wait(&full[s], ph, wc);
-        }
-        for (int j = tiles_issued > 2 ? tiles_issued - 2 : 0; j < tiles_issued; ++j)
-          (void)mbar_wait(&pfull[j & 1], uint32_t(j >> 1) & 1u, wc);
-      }
+      issued_by[0] = uint32_t(issued);
+      issued_by[1] = uint32_t(tiles_issued);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
@@ -1114,6 +1126,14 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
 
   tc_fence_before();
   __syncthreads();
+  // after a give-up, whoever gave up, the copies in flight land before the CTA
+  // can exit
+  if (*abort_flag && threadIdx.x == 0) {
+    const int n = int(issued_by[0]);
+    for (int i = n > C::STAGES ? n - C::STAGES : 0; i < n; ++i)
+      (void)mbar_wait(&full[i % C::STAGES], uint32_t(i / C::STAGES) & 1u, wc);
+    wait_param_copies(pfull, issued_by[1], wc);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -1190,7 +1210,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   uint64_t* rbar = drain + 1;  // [EPW] box of the residual arrived (wide epilogue)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + (C::WIDE ? C::EPW : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* issued_by = tmem_slot + 2;  // [2], rank 0: stages each CTA loaded
+  // [0], [1] (rank 0): stages each CTA loaded; [2]: parameter slots this CTA loaded
+  uint32_t* issued_by = tmem_slot + 2;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1265,10 +1286,12 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
-          const uint32_t bar = full0 + uint32_t(stage) * 8u;
-          tma_load_2d_pair(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, a_row, bar);
-          tma_load_2d_pair(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, b_row, bar);
+          if (!withheld<EP>(p, issued)) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+            const uint32_t bar = full0 + uint32_t(stage) * 8u;
+            tma_load_2d_pair(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, a_row, bar);
+            tma_load_2d_pair(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, b_row, bar);
+          }
           ++issued;
           if (++stage == C::STAGES) {
             stage = 0;
@@ -1276,10 +1299,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
           }
         }
       }
-      if (!ok) {
-        for (int j = tiles_issued > 2 ? tiles_issued - 2 : 0; j < tiles_issued; ++j)
-          (void)mbar_wait(&pfull[j & 1], uint32_t(j >> 1) & 1u, wc);
-      }
+      issued_by[2] = uint32_t(tiles_issued);
       st_shared_cluster_u32(mapa_shared(&issued_by[rank], 0), uint32_t(issued));
     }
   } else if (warp == 1) {
@@ -1433,6 +1453,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both producers have posted their stage counts
+  // after a give-up, whoever gave up, the parameter copies in flight land too
+  if (*abort_flag && threadIdx.x == 32) wait_param_copies(pfull, issued_by[2], wc);
   if (rank == 0 && threadIdx.x == 0) {
     // every stage copy of either CTA lands before either CTA can exit
     const int L = int(issued_by[0]), P = int(issued_by[1]);

@@ -131,7 +131,9 @@ struct GemmEpParams : GemmParams {
   const uint16_t* gate;      // bf16 [ceil(T / gate_rows), N] or null
   int64_t gate_rows;         // rows of Y per row of the gate
   const uint16_t* bias16;    // bf16 operands: bf16 bias [N] or null (p.bias is null)
+  int withhold;              // test hook: 0, or a copy that each CTA leaves out
 };
+constexpr int kWithholdStage = 1, kWithholdResidual = 2;  // its first stage; its first boxes of R
 
 // As launch_gemm / launch_gemm_pair.  maps: four CUtensorMap, A and B as there,
 // then Y and the residual (without one: any map) [T,N] bf16 with box {64, 32}

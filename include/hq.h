@@ -307,9 +307,20 @@ hq_status hq_debug_set_gemm_variant(int variant);
  *       an epilogue that split K over a cluster (hq_ops.h), the copy of the
  *       first operand stage is never issued, so the tensor cores' bounded wait
  *       for it expires.  The kernel records HQ_ERR_TIMEOUT, waits for the
- *       copies it did issue and exits.
+ *       copies it did issue and exits;
+ *   HQ_FAULT_TILE_WITHHOLD_STAGE (3)     the same in the products with an
+ *       epilogue that take whole output tiles;
+ *   HQ_FAULT_TILE_WITHHOLD_RESIDUAL (4)  there the copy of each epilogue warp's
+ *       first box of the residual (with tiles of up to 192 columns; wider ones
+ *       read the residual without a wait).
  * Host state, applies to launches issued after the call. */
-enum { HQ_FAULT_NONE = 0, HQ_FAULT_QUANT_WITHHOLD_ROW = 1, HQ_FAULT_SPLITK_WITHHOLD_STAGE = 2 };
+enum {
+  HQ_FAULT_NONE = 0,
+  HQ_FAULT_QUANT_WITHHOLD_ROW = 1,
+  HQ_FAULT_SPLITK_WITHHOLD_STAGE = 2,
+  HQ_FAULT_TILE_WITHHOLD_STAGE = 3,
+  HQ_FAULT_TILE_WITHHOLD_RESIDUAL = 4
+};
 hq_status hq_debug_inject_fault(int kind);
 
 /* Test hook, host only (no device call, usable without a GPU): the launch

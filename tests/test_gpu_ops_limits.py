@@ -81,3 +81,24 @@ def test_split_k_gives_up_and_recovers(hq, make, T, K, N):
     """A stage of the K split that never comes, where the producer has issued all
     its copies and left (few K blocks a CTA) and where it waits for a free stage."""
     _times_out_and_recovers(hq, *make(hq, T, K, N), hq.HQ_FAULT_SPLITK_WITHHOLD_STAGE)
+
+
+# one output tile a CTA and several, one CTA a tile and pairs of them, few K
+# blocks (the producer has left) and many
+TILES = [(_dense, 600, 1152, 1152), (_dense, 4100, 512, 1152), (_dense, 7000, 4608, 1152),
+         (_dense, 4096, 4608, 4608), (_linear, 2000, 320, 320), (_linear, 8192, 4608, 1152),
+         (_linear, 4096, 4608, 4608)]
+
+
+@pytest.mark.parametrize("make,T,K,N", TILES)
+def test_tiles_give_up_and_recover(hq, make, T, K, N):
+    """A stage of a tile kernel's main loop that never comes."""
+    _times_out_and_recovers(hq, *make(hq, T, K, N), hq.HQ_FAULT_TILE_WITHHOLD_STAGE)
+
+
+# tiles of 256 columns read the residual without a wait
+@pytest.mark.parametrize("make,T,K,N", [(_dense, 600, 1152, 1152), (_dense, 4100, 512, 1152),
+                                        (_linear, 2000, 320, 320), (_linear, 8192, 4608, 1152)])
+def test_residual_box_gives_up_and_recovers(hq, make, T, K, N):
+    """A box of the residual that never comes."""
+    _times_out_and_recovers(hq, *make(hq, T, K, N), hq.HQ_FAULT_TILE_WITHHOLD_RESIDUAL)

@@ -180,6 +180,8 @@ def test_a_reused_epilogue_forgets_tensors_taken_away(hq):
 
 def test_known_faults_only(hq):
     lib = hq.load_library()
-    assert lib.hq_debug_inject_fault(hq.HQ_FAULT_SPLITK_WITHHOLD_STAGE) == OK
+    for kind in (hq.HQ_FAULT_SPLITK_WITHHOLD_STAGE, hq.HQ_FAULT_TILE_WITHHOLD_STAGE,
+                 hq.HQ_FAULT_TILE_WITHHOLD_RESIDUAL):
+        assert lib.hq_debug_inject_fault(kind) == OK
     assert lib.hq_debug_inject_fault(hq.HQ_FAULT_NONE) == OK
     assert lib.hq_debug_inject_fault(-1) == INVALID and lib.hq_debug_inject_fault(100) == INVALID
