@@ -480,6 +480,7 @@ class _Runtime:
         self.bf16, self.f32, self.i8 = torch.bfloat16, torch.float32, torch.int8
         self.u8, self.i32 = torch.uint8, torch.int32
         self.device_guard = torch.cuda.device
+        self.capturing = torch.cuda.is_current_stream_capturing
         self.current_device = torch.cuda.current_device
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream_of = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -610,7 +611,47 @@ def hq_group_norm(desc: GroupNormDesc, X, gamma, beta, Y, workspace=None, stream
 # one layer's caller-side buffers
 # ---------------------------------------------------------------------------
 
-class HadamardQuantLinear:
+class _ActivationBuffers:
+    """The activation buffers of a quantized layer (codes, scales, workspace):
+    a set for each token count and stream, since calls on two streams may
+    overlap and each writes its set between the quantizer and the product.
+    Sets that a caller asked for (buffers, quantize) stay for the layer's life;
+    of those that forward took for itself the last KEPT_SETS used do.  A forward
+    that is being captured takes memory of its graph's own instead, so that two
+    graphs may be replayed at once."""
+
+    KEPT_SETS = 8
+
+    def _stream_key(self):
+        """The current stream of the layer's device."""
+        dev = self.w_codes.get_device()
+        return None if dev < 0 else _runtime().stream_of(dev)
+
+    def _set_for(self, T, asked):
+        key = (T, self._stream_key())
+        with _buffers_lock:
+            b, was_asked = self._bufs.pop(key, (None, False))
+            if b is None:
+                b = self._new_buffers(T)
+            self._bufs[key] = (b, asked or was_asked)  # the newest, last
+            own = [k for k, (_, kept) in self._bufs.items() if not kept]
+            if len(own) > self.KEPT_SETS:
+                del self._bufs[own[0]]
+        return b
+
+    def buffers(self, T: int):
+        """The set that calls with T tokens on the current stream use."""
+        return self._set_for(T, True)
+
+    def _call_buffers(self, T: int):
+        """The set of one forward call."""
+        return self._new_buffers(T) if _runtime().capturing() else self._set_for(T, False)
+
+
+_buffers_lock = threading.Lock()
+
+
+class HadamardQuantLinear(_ActivationBuffers):
     """Prepared weights and activation buffers of one Hadamard-domain layer.
 
     Allocation is the caller's (PyTorch); the library only reads and writes the
@@ -638,23 +679,21 @@ class HadamardQuantLinear:
         self.workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=dev) if ws else None
         self._bufs = {}
 
-    def buffers(self, T: int):
+    def _new_buffers(self, T: int):
         import torch
-        b = self._bufs.get(T)
-        if b is None:
-            dev = self.w_codes.device
-            per_row = self.desc.act_gran == HQ_PER_TOKEN
-            if self.desc.code_format == HQ_CODES_I4_PACKED:  # two codes per byte
-                codes = torch.empty((T, self.desc.K // 2), dtype=torch.uint8, device=dev)
-            else:
-                codes = torch.empty((T, self.desc.K), dtype=torch.int8, device=dev)
-            b = {"a_codes": codes,
-                 "a_scale": torch.empty(T if per_row else 1, dtype=torch.float32, device=dev),
-                 "a_mean": torch.empty(T, dtype=torch.float32, device=dev)}
-            if self.desc.act_gran == HQ_PER_TENSOR_STATIC:
-                # an input of the quantizer and of the GEMM in this mode
-                b["a_scale"].fill_(self.static_scale)
-            self._bufs[T] = b
+        dev = self.w_codes.device
+        per_row = self.desc.act_gran == HQ_PER_TOKEN
+        if self.desc.code_format == HQ_CODES_I4_PACKED:  # two codes per byte
+            codes = torch.empty((T, self.desc.K // 2), dtype=torch.uint8, device=dev)
+        else:
+            codes = torch.empty((T, self.desc.K), dtype=torch.int8, device=dev)
+        b = {"a_codes": codes,
+             "a_scale": torch.empty(T if per_row else 1, dtype=torch.float32, device=dev),
+             "a_mean": torch.empty(T, dtype=torch.float32, device=dev),
+             "workspace": None if self.workspace is None else torch.empty_like(self.workspace)}
+        if self.desc.act_gran == HQ_PER_TENSOR_STATIC:
+            # an input of the quantizer and of the GEMM in this mode
+            b["a_scale"].fill_(self.static_scale)
         return b
 
     @staticmethod
@@ -670,10 +709,11 @@ class HadamardQuantLinear:
             raise ValueError("static_scale is only used with HQ_PER_TENSOR_STATIC")
         return None
 
-    def quantize(self, X):
-        b = self.buffers(X.shape[0])
+    def quantize(self, X, bufs=None):
+        """Quantizes X into `bufs` (None: buffers(T)) and returns them."""
+        b = self.buffers(X.shape[0]) if bufs is None else bufs
         hq_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, b["a_codes"],
-                        b["a_scale"], b["a_mean"], self.workspace)
+                        b["a_scale"], b["a_mean"], b["workspace"])
         return b
 
     def forward(self, X, Y=None, acc_debug=None, epilogue=None):
@@ -682,7 +722,7 @@ class HadamardQuantLinear:
         T = X.shape[0]
         if Y is None:
             Y = torch.empty((T, self.desc.N), dtype=torch.bfloat16, device=X.device)
-        b = self.quantize(X)
+        b = self.quantize(X, self._call_buffers(T))
         mean = b["a_mean"] if self.desc.centering != HQ_CENTER_NONE else None
         if epilogue is not None:
             hq_linear_ep(self.desc, b["a_codes"], b["a_scale"], mean, self.w_codes, self.w_scale,
@@ -697,7 +737,7 @@ class HadamardQuantLinear:
     def forward_host(self, X_host, Y_host=None, chunks=8):
         """Y_host = the layer on X_host (pinned CPU bf16 tensors), with the
         uploads, kernels and downloads of `chunks` row chunks overlapped
-        (hq_forward_host).  Device staging buffers are kept per token count."""
+        (hq_forward_host).  Device staging buffers are kept with buffers(T)."""
         import torch
         T = X_host.shape[0]
         b = self.buffers(T)
@@ -708,7 +748,7 @@ class HadamardQuantLinear:
         if Y_host is None:
             Y_host = torch.empty((T, self.desc.N), dtype=torch.bfloat16).pin_memory()
         hq_forward_host(self.desc, X_host, b["X_dev"], self.sigma_inv if self.use_sigma else None,
-                        b["a_codes"], b["a_scale"], b["a_mean"], self.workspace, self.w_codes,
+                        b["a_codes"], b["a_scale"], b["a_mean"], b["workspace"], self.w_codes,
                         self.w_scale, self.colsum, self.bias_f32, b["Y_dev"], Y_host, chunks)
         return Y_host
 
@@ -807,7 +847,7 @@ class HadamardQuantLinear:
         return self
 
 
-class GroupWiseQuantLinear:
+class GroupWiseQuantLinear(_ActivationBuffers):
     """Prepared weights and activation buffers of one group-wise layer
     (include/hq_gw.h): 64-channel groups, each with its own H_64 block and
     scale, and a rank-`rank` 16-bit branch.  `forward(X)` =
@@ -863,23 +903,20 @@ class GroupWiseQuantLinear:
                               self.w_codes, self.w_scale, self.l1s, self.l2b, self.bias_f32)
         self._bufs = {}
 
-    def buffers(self, T: int):
+    def _new_buffers(self, T: int):
         import torch
-        b = self._bufs.get(T)
-        if b is None:
-            dev = self.w_codes.device
-            K, r = self.desc.K, self.desc.rank
-            ws = hq_gw_quantize_act_workspace_bytes(self.desc, T)
-            b = {"a_codes": torch.empty((T, K), dtype=torch.float8_e4m3fn, device=dev),
-                 "a_scale": torch.empty((K // 64, hq_gw_scale_ld(T)), dtype=torch.float32,
-                                        device=dev),
-                 "u": torch.empty((T, r), dtype=torch.bfloat16, device=dev) if r else None,
-                 "workspace": torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None}
-            self._bufs[T] = b
-        return b
+        dev = self.w_codes.device
+        K, r = self.desc.K, self.desc.rank
+        ws = hq_gw_quantize_act_workspace_bytes(self.desc, T)
+        return {"a_codes": torch.empty((T, K), dtype=torch.float8_e4m3fn, device=dev),
+                "a_scale": torch.empty((K // 64, hq_gw_scale_ld(T)), dtype=torch.float32,
+                                       device=dev),
+                "u": torch.empty((T, r), dtype=torch.bfloat16, device=dev) if r else None,
+                "workspace": torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None}
 
-    def quantize(self, X):
-        b = self.buffers(X.shape[0])
+    def quantize(self, X, bufs=None):
+        """Quantizes X into `bufs` (None: buffers(T)) and returns them."""
+        b = self.buffers(X.shape[0]) if bufs is None else bufs
         hq_gw_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, self.l1s,
                            b["a_codes"], b["a_scale"], b["u"], b["workspace"])
         return b
@@ -888,7 +925,7 @@ class GroupWiseQuantLinear:
         import torch
         if Y is None:
             Y = torch.empty((X.shape[0], self.desc.N), dtype=torch.bfloat16, device=X.device)
-        b = self.quantize(X)
+        b = self.quantize(X, self._call_buffers(X.shape[0]))
         hq_gw_linear(self.desc, b["a_codes"], b["a_scale"], b["u"], self.w_codes, self.w_scale,
                      self.l2b, self.bias_f32, Y, T=X.shape[0])
         return Y

@@ -185,3 +185,41 @@ def test_known_faults_only(hq):
         assert lib.hq_debug_inject_fault(kind) == OK
     assert lib.hq_debug_inject_fault(hq.HQ_FAULT_NONE) == OK
     assert lib.hq_debug_inject_fault(-1) == INVALID and lib.hq_debug_inject_fault(100) == INVALID
+
+
+def _bare_layer(hq):
+    """A layer with weights of no use, in host memory: its bookkeeping alone."""
+    torch = pytest.importorskip("torch")
+    lay = hq.HadamardQuantLinear.__new__(hq.HadamardQuantLinear)
+    lay.desc = hq.LayerDesc(64, 32, 16, act_gran=hq.HQ_PER_TENSOR_DYNAMIC)
+    lay.w_codes = torch.zeros((32, 64), dtype=torch.int8)
+    lay.workspace = torch.empty(16, dtype=torch.uint8)
+    lay._bufs = {}
+    return lay
+
+
+def test_activation_buffers_of_two_streams_share_no_memory(hq):
+    """Calls with the same number of tokens on two streams may run at once: each
+    stream has codes, scale, mean and workspace of its own, found again."""
+    lay, stream = _bare_layer(hq), [1]
+    lay._stream_key = lambda: stream[0]
+    one = lay.buffers(5)
+    stream[0] = 2
+    two = lay.buffers(5)
+    for name in ("a_codes", "a_scale", "a_mean", "workspace"):
+        assert one[name].data_ptr() != two[name].data_ptr(), name
+    assert lay.buffers(5) is two
+    stream[0] = 1
+    assert lay.buffers(5) is one and lay.buffers(6) is not one
+
+
+def test_activation_buffers_of_many_token_counts_are_bounded(hq):
+    """What forward takes for itself is given back after other token counts; what
+    a caller asked for stays."""
+    lay = _bare_layer(hq)
+    asked = lay.buffers(1000)
+    for T in range(1, 100):
+        lay._set_for(T, False)
+    assert len(lay._bufs) == lay.KEPT_SETS + 1
+    last = lay._set_for(99, False)
+    assert lay.buffers(99) is last and lay.buffers(1000) is asked
