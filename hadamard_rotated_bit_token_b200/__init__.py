@@ -34,6 +34,7 @@ quantized 1x1 convolution it feeds.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -651,6 +652,25 @@ class _ActivationBuffers:
 _buffers_lock = threading.Lock()
 
 
+def _on_layer_device(method):
+    """A method of a layer run with the layer's device current, so that every
+    launch of it goes to that device's current stream."""
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        rt, dev = _rt or _runtime(), self.w_codes.get_device()
+        if dev < 0 or rt.current_device() == dev:
+            return method(self, *args, **kwargs)
+        with rt.device_guard(dev):
+            return method(self, *args, **kwargs)
+    return call
+
+
+def _check_input_device(layer, X):
+    if X.get_device() != layer.w_codes.get_device():
+        raise ValueError(f"X must live on the layer's device {layer.w_codes.device}, "
+                         f"got {X.device}")
+
+
 class HadamardQuantLinear(_ActivationBuffers):
     """Prepared weights and activation buffers of one Hadamard-domain layer.
 
@@ -709,13 +729,16 @@ class HadamardQuantLinear(_ActivationBuffers):
             raise ValueError("static_scale is only used with HQ_PER_TENSOR_STATIC")
         return None
 
+    @_on_layer_device
     def quantize(self, X, bufs=None):
         """Quantizes X into `bufs` (None: buffers(T)) and returns them."""
+        _check_input_device(self, X)
         b = self.buffers(X.shape[0]) if bufs is None else bufs
         hq_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, b["a_codes"],
                         b["a_scale"], b["a_mean"], b["workspace"])
         return b
 
+    @_on_layer_device
     def forward(self, X, Y=None, acc_debug=None, epilogue=None):
         """epilogue: an Epilogue for the product's output (hq_linear_ep)."""
         import torch
@@ -734,6 +757,7 @@ class HadamardQuantLinear(_ActivationBuffers):
 
     __call__ = forward
 
+    @_on_layer_device
     def forward_host(self, X_host, Y_host=None, chunks=8):
         """Y_host = the layer on X_host (pinned CPU bf16 tensors), with the
         uploads, kernels and downloads of `chunks` row chunks overlapped
@@ -914,13 +938,16 @@ class GroupWiseQuantLinear(_ActivationBuffers):
                 "u": torch.empty((T, r), dtype=torch.bfloat16, device=dev) if r else None,
                 "workspace": torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None}
 
+    @_on_layer_device
     def quantize(self, X, bufs=None):
         """Quantizes X into `bufs` (None: buffers(T)) and returns them."""
+        _check_input_device(self, X)
         b = self.buffers(X.shape[0]) if bufs is None else bufs
         hq_gw_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, self.l1s,
                            b["a_codes"], b["a_scale"], b["u"], b["workspace"])
         return b
 
+    @_on_layer_device
     def forward(self, X, Y=None):
         import torch
         if Y is None:

@@ -223,3 +223,56 @@ def test_activation_buffers_of_many_token_counts_are_bounded(hq):
     assert len(lay._bufs) == lay.KEPT_SETS + 1
     last = lay._set_for(99, False)
     assert lay.buffers(99) is last and lay.buffers(1000) is asked
+
+
+def test_a_layers_launches_all_go_to_its_own_device(hq, monkeypatch):
+    """A layer on device 1 called while device 0 is current: the quantizer and the
+    product both run with device 1 current, and device 0 is current again after."""
+    torch = pytest.importorskip("torch")
+    current, seen = [0], []
+
+    class Guard:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.old
+
+    rt = type("Runtime", (), dict(
+        current_device=staticmethod(lambda: current[0]), device_guard=Guard,
+        stream_of=staticmethod(lambda dev: 100 + dev), capturing=staticmethod(lambda: False)))
+    monkeypatch.setattr(hq, "_rt", rt)
+    for name in ("hq_quantize_act", "hq_linear", "hq_linear_ep", "hq_gw_quantize_act",
+                 "hq_gw_linear"):
+        monkeypatch.setattr(hq, name, lambda *a, _n=name, **k: seen.append((_n, current[0])))
+
+    class On1(_OnDevice):
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    X = On1(FAKE, (4, 64), torch.bfloat16)
+    lay = _bare_layer(hq)
+    lay.use_sigma, lay.w_scale, lay.colsum, lay.bias_f32 = False, None, None, None
+    gw = hq.GroupWiseQuantLinear.__new__(hq.GroupWiseQuantLinear)
+    gw.desc, gw._bufs, gw.use_sigma = hq.GwDesc(64, 32, 64, 0), {}, False
+    gw.l1s = gw.l2b = gw.w_scale = gw.bias_f32 = None
+    for layer in (lay, gw):
+        layer.w_codes = On1(FAR, (32, 64), torch.int8)
+        layer._new_buffers = lambda T: dict.fromkeys(
+            ("a_codes", "a_scale", "a_mean", "u", "workspace"))
+    Y = On1(2 * FAR, (4, 32), torch.bfloat16)
+    lay.forward(X, Y)
+    lay.forward(X, Y, epilogue=hq.Epilogue(hq.HQ_ACT_SILU))
+    gw.forward(X, Y)
+    assert seen == [("hq_quantize_act", 1), ("hq_linear", 1), ("hq_quantize_act", 1),
+                    ("hq_linear_ep", 1), ("hq_gw_quantize_act", 1), ("hq_gw_linear", 1)]
+    assert current == [0] and all(key == (4, 101) for key in lay._bufs)
+    # an input on another device than the layer's is refused
+    for layer in (lay, gw):
+        with pytest.raises(ValueError, match="device"):
+            layer.forward(torch.zeros(4, 64, dtype=torch.bfloat16), Y)
