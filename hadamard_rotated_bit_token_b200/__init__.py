@@ -57,6 +57,9 @@ __all__ = [
     "HQ_ACT_NONE", "HQ_ACT_RELU", "HQ_ACT_SILU", "HQ_ACT_GELU", "HQ_ACT_GELU_TANH", "Epilogue",
     "DenseDesc", "GroupNormDesc", "hq_linear_ep", "hq_dense", "hq_group_norm",
     "hq_group_norm_workspace_bytes", "DenseLinear", "GroupNorm", "PointwiseBlock",
+    "HQ_PRODUCT_AUTO", "HQ_PRODUCT_ROWS", "HQ_PRODUCT_SPLIT", "HQ_PRODUCT_TILES",
+    "HQ_PRODUCT_PAIR", "HQ_PRODUCT_LINEAR", "ProductPlan", "hq_debug_dense_plan",
+    "hq_debug_linear_ep_plan", "hq_debug_set_product_plan",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +72,8 @@ HQ_FAULT_NONE, HQ_FAULT_QUANT_WITHHOLD_ROW, HQ_FAULT_SPLITK_WITHHOLD_STAGE = 0, 
 HQ_FAULT_TILE_WITHHOLD_STAGE, HQ_FAULT_TILE_WITHHOLD_RESIDUAL = 3, 4
 HQ_GEMM_AUTO, HQ_GEMM_SINGLE_CTA, HQ_GEMM_CTA_PAIR = 0, 1, 2
 HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_ACT_GELU, HQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
+HQ_PRODUCT_AUTO, HQ_PRODUCT_ROWS, HQ_PRODUCT_SPLIT, HQ_PRODUCT_TILES = 0, 1, 2, 3
+HQ_PRODUCT_PAIR, HQ_PRODUCT_LINEAR = 4, 5
 STATUS_NAMES = {0: "HQ_OK", 1: "HQ_ERR_INVALID_ARGUMENT", 2: "HQ_ERR_UNSUPPORTED",
                 3: "HQ_ERR_MISALIGNED", 4: "HQ_ERR_CUDA", 5: "HQ_ERR_TIMEOUT",
                 6: "HQ_ERR_DEVICE"}
@@ -80,7 +85,8 @@ EXPORTED = ("hq_status_string", "hq_version", "hq_calib_act_absmax", "hq_prepare
             "hq_gw_prepare_weights", "hq_gw_quantize_act", "hq_gw_linear",
             "hq_gw_debug_linear_f32", "hq_debug_last_cuda_error",
             "hq_gw_quantize_act_workspace_bytes", "hq_linear_ep", "hq_dense", "hq_group_norm",
-            "hq_group_norm_workspace_bytes")
+            "hq_group_norm_workspace_bytes", "hq_debug_dense_plan", "hq_debug_linear_ep_plan",
+            "hq_debug_set_product_plan")
 
 
 class HQError(RuntimeError):
@@ -128,6 +134,17 @@ class GroupNormDesc(ctypes.Structure):
 
     def __init__(self, C, groups, act=HQ_ACT_NONE, eps=1e-5):
         super().__init__(C, groups, act, eps)
+
+
+class ProductPlan(ctypes.Structure):
+    """hq_product_plan (host memory): the kernel of a product with an epilogue."""
+    _fields_ = [("kernel", ctypes.c_int32), ("width", ctypes.c_int32), ("split", ctypes.c_int32)]
+
+    def __init__(self, kernel=HQ_PRODUCT_AUTO, width=1, split=1):
+        super().__init__(kernel, width, split)
+
+    def __iter__(self):
+        return iter((self.kernel, self.width, self.split))
 
 
 class Epilogue(ctypes.Structure):
@@ -221,7 +238,14 @@ def load_library():
         lib.hq_group_norm_workspace_bytes.restype = ctypes.c_size_t
         lib.hq_group_norm.argtypes = [gn_p, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp,
                                       _vp, ctypes.c_size_t, _vp]
-        for name in ("hq_linear_ep", "hq_dense", "hq_group_norm"):
+        plan_p = ctypes.POINTER(ProductPlan)
+        lib.hq_debug_dense_plan.argtypes = [ctypes.POINTER(DenseDesc), ctypes.c_int64, ctypes.c_int,
+                                            ctypes.c_int, ctypes.c_int, plan_p]
+        lib.hq_debug_linear_ep_plan.argtypes = [desc_p, ctypes.c_int64] + [ctypes.c_int] * 4 + [
+            plan_p]
+        lib.hq_debug_set_product_plan.argtypes = [plan_p]
+        for name in ("hq_linear_ep", "hq_dense", "hq_group_norm", "hq_debug_dense_plan",
+                     "hq_debug_linear_ep_plan", "hq_debug_set_product_plan"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("hq_calib_act_absmax", "hq_prepare_weights", "hq_quantize_act", "hq_linear",
                      "hq_forward_host",
@@ -583,6 +607,31 @@ def hq_dense(desc: DenseDesc, X, W, bias, epilogue, Y, stream=None):
             _tensor(X, "X", bf16, (T, K), dev), T, _tensor(W, "W", bf16, (N, K), dev),
             _tensor(bias, "bias", bf16, (N,), dev), _epilogue_ref(rt, epilogue, T, N, dev),
             _tensor(Y, "Y", bf16, (T, N), dev))
+
+
+def hq_debug_dense_plan(desc: DenseDesc, T: int, act=HQ_ACT_NONE, sms=148,
+                        pair_clusters=74) -> ProductPlan:
+    """The kernel that hq_dense takes (host only)."""
+    plan = ProductPlan()
+    _check(load_library().hq_debug_dense_plan(ctypes.byref(desc), T, act, sms, pair_clusters,
+                                              ctypes.byref(plan)), "hq_debug_dense_plan")
+    return plan
+
+
+def hq_debug_linear_ep_plan(desc: LayerDesc, T: int, act=HQ_ACT_NONE, plain=False, sms=148,
+                            pair_clusters=74) -> ProductPlan:
+    """The kernel that hq_linear_ep takes (host only)."""
+    plan = ProductPlan()
+    _check(load_library().hq_debug_linear_ep_plan(ctypes.byref(desc), T, int(plain), act, sms,
+                                                  pair_clusters, ctypes.byref(plan)),
+           "hq_debug_linear_ep_plan")
+    return plan
+
+
+def hq_debug_set_product_plan(plan: ProductPlan = None):
+    """hq_dense and hq_linear_ep take this kernel (None: they choose)."""
+    _check(load_library().hq_debug_set_product_plan(None if plan is None else ctypes.byref(plan)),
+           "hq_debug_set_product_plan")
 
 
 def hq_group_norm_workspace_bytes(desc: GroupNormDesc, B: int, S: int) -> int:

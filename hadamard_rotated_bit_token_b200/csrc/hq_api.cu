@@ -47,6 +47,7 @@ EncodeTiledFn g_encode = nullptr;
 unsigned long long g_wait_ns = 0;  // 0 -> default
 int g_fault = 0;
 int g_gemm_variant = 0;  // HQ_GEMM_AUTO
+hq_product_plan g_product_plan = {};  // HQ_PRODUCT_AUTO
 
 unsigned long long wait_ns() { return g_wait_ns ? g_wait_ns : 2000000000ull; }
 int injected_fault() {
@@ -865,22 +866,23 @@ void set_rows_epilogue(Params* p, const hq_epilogue* ep, uint16_t* Y) {
 
 // Launches hq_splitk.cu's kernel on [T, row_bytes] by [N, row_bytes] operands;
 // the epilogue and scales of p are set.
-hq_status run_splitk(const DeviceState* dev, const SplitKPlan& pl, bool bf16, const void* A,
+hq_status run_splitk(const DeviceState* dev, const hq_product_plan& pl, bool bf16, const void* A,
                      int64_t T, const void* B, int N, int row_bytes, SplitKParams* p,
                      cudaStream_t st) {
   CUtensorMap tx, tw;
-  hq_status s = encode_kmajor_i8(&tx, A, T, row_bytes, pl.nt);
+  hq_status s = encode_kmajor_i8(&tx, A, T, row_bytes, pl.width);
   if (s != HQ_OK) return s;
   if ((s = encode_kmajor_i8(&tw, B, N, row_bytes, 128)) != HQ_OK) return s;
   p->T = T;
   p->N = N;
-  p->log_split = pl.log_split;
-  p->k_blocks = pl.k_blocks;
+  p->log_split = ilog2_exact(pl.split);
+  p->k_blocks = (row_bytes + 127) / 128;
   p->num_n_tiles = (N + 127) / 128;
   p->err = dev->err;
   p->wait_ns = wait_ns();
   p->withhold = injected_fault() == HQ_FAULT_SPLITK_WITHHOLD_STAGE;
-  return from_cuda(launch_splitk(bf16, pl.nt, &tx, &tw, *p, pl.tiles, st));
+  return from_cuda(launch_splitk(bf16, pl.width, &tx, &tw, *p,
+                                 int(splitk_tiles(T, N, pl.width)), st));
 }
 
 bool plain_epilogue(const hq_epilogue* ep) {
@@ -901,12 +903,94 @@ int pair_clusters(DeviceState* dev) {
   return dev->pair_clusters;
 }
 
+// What the choice of a product's kernel goes by.
+struct ProductShape {
+  int64_t T;
+  int N;
+  int64_t row_bytes;  // of the weights
+  bool bf16, packed;  // bf16 operands; packed activation codes
+  int logo;           // log2 of the weight-only form's output blocks (0: none)
+  bool act, plain;    // an activation; no epilogue at all
+  bool acc_debug;     // raw accumulators asked for
+};
+
+// The kernel for a product with an epilogue: the hook's where it is set (and
+// can run this product), else a few tokens by one pass over the weights, too few
+// tiles for the GPU by a K split, whichever is modelled faster, or tiles.  Raw
+// accumulators and the weight-only form's transform need the tiles; packed codes
+// have no K split.
+hq_status plan_product(const ProductShape& q, int sms, int pair_clusters, hq_product_plan* out) {
+  const bool tiles_only = q.logo > 0 || q.acc_debug;
+  hq_product_plan forced;
+  int variant;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    forced = g_product_plan;
+    variant = g_gemm_variant;
+  }
+  const int rows_t = q.T <= 1 ? 1 : q.T <= 2 ? 2 : q.T <= 4 ? 4 : 8;
+  const hq_product_plan rows{HQ_PRODUCT_ROWS, rows_t,
+                             q.T <= kRowsMaxT ? rows_warps(int(q.T), q.N, q.row_bytes, sms) : 0};
+  if (forced.kernel != HQ_PRODUCT_AUTO) {
+    const bool wide_pair = forced.kernel == HQ_PRODUCT_PAIR;
+    bool can = false;
+    switch (forced.kernel) {
+      case HQ_PRODUCT_ROWS: can = q.T <= kRowsMaxT && !tiles_only; break;
+      case HQ_PRODUCT_SPLIT:
+        can = !tiles_only && !q.packed && (q.row_bytes + 127) / 128 >= forced.split &&
+              splitk_tiles(q.T, q.N, forced.width) * forced.split < (int64_t(1) << 31);
+        break;
+      case HQ_PRODUCT_TILES:
+      case HQ_PRODUCT_PAIR:
+        can = wide_pair ? pair_clusters > 0 && q.logo == 0 && !q.packed
+                        : !q.packed || forced.width <= 192;
+        break;
+    }
+    if (!can) return HQ_ERR_UNSUPPORTED;
+    *out = forced.kernel == HQ_PRODUCT_ROWS ? rows : forced;
+    return HQ_OK;
+  }
+  if (!tiles_only && few_tokens(q.T, q.N, q.row_bytes, q.packed)) {
+    *out = rows;
+    return HQ_OK;
+  }
+  double tiles_us;
+  const GemmChoice gc = choose_gemm_ep(q.T, q.N, q.row_bytes, sms, pair_clusters, q.logo, q.packed,
+                                       q.act, &tiles_us);
+  if (!tiles_only && !q.packed) {
+    const SplitKPlan pl = splitk_plan(q.T, q.N, q.row_bytes, sms);
+    if (pl.us < tiles_us) {
+      *out = hq_product_plan{HQ_PRODUCT_SPLIT, pl.nt, 1 << pl.log_split};
+      return HQ_OK;
+    }
+  }
+  if (q.plain && !q.bf16) {  // hq_linear's own kernels
+    const GemmChoice g = choose_gemm(q.T, q.N, int(q.row_bytes), sms, pair_clusters, variant,
+                                     q.logo, q.packed);
+    *out = hq_product_plan{HQ_PRODUCT_LINEAR, g.bn, g.pair ? 2 : 1};
+    return HQ_OK;
+  }
+  // (the GEMM hook of hq_linear holds for its product with an epilogue too)
+  const GemmChoice g = variant == HQ_GEMM_AUTO || q.bf16
+                           ? gc
+                           : choose_gemm(q.T, q.N, int(q.row_bytes), sms, pair_clusters, variant,
+                                         q.logo, q.packed);
+  *out = hq_product_plan{g.pair ? HQ_PRODUCT_PAIR : HQ_PRODUCT_TILES, g.bn, 1};
+  return HQ_OK;
+}
+
+ProductShape shape_of(const hq_layer_desc* d, int64_t T, bool plain, bool act, bool acc_debug) {
+  return ProductShape{T, d->N, d->K, false, d->code_format == HQ_CODES_I4_PACKED,
+                      ilog2_exact(d->out_order > 1 ? d->out_order : 1), act, plain, acc_debug};
+}
+
 // The integer GEMM behind hq_linear and hq_linear_ep (arguments checked, T > 0);
-// `ep` is null for the plain epilogue.
+// `ep` is null for the plain epilogue, else `ep_choice` is its tile.
 hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
                       const float* a_scale, const float* a_mean, const int8_t* w_codes,
                       const float* w_scale, const float* colsum, const float* bias_f32,
-                      const hq_epilogue* ep, uint16_t* Y, int32_t* acc_debug, hq_stream_t stream) {
+                      const hq_epilogue* ep, const GemmChoice& ep_choice, uint16_t* Y,
+                      int32_t* acc_debug, hq_stream_t stream) {
   hq_status s;
   DeviceState* dev;
   s = device_state(&dev);
@@ -924,10 +1008,8 @@ hq_status linear_impl(const hq_layer_desc* desc, int64_t T, const int8_t* a_code
   const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
   if (variant == HQ_GEMM_CTA_PAIR && clusters_max <= 0 && logo == 0) return HQ_ERR_UNSUPPORTED;
   const GemmChoice gc =
-      ep != nullptr && variant == HQ_GEMM_AUTO
-          ? choose_gemm_ep(T, N, K, dev->sm_count, clusters_max, logo, packed,
-                           ep->act != HQ_ACT_NONE, nullptr)
-          : choose_gemm(T, N, K, dev->sm_count, clusters_max, variant, logo, packed);
+      ep != nullptr ? ep_choice
+                    : choose_gemm(T, N, K, dev->sm_count, clusters_max, variant, logo, packed);
   const int bn = gc.bn;
   CUtensorMap maps[4];
   CUtensorMap &ta = maps[0], &tb = maps[1], &ty = maps[2];
@@ -1292,7 +1374,7 @@ hq_status hq_linear(const hq_layer_desc* desc, int64_t T, const int8_t* a_codes,
                                         bias_f32, Y, acc_debug);
   if (s != HQ_OK || T == 0) return s;
   return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
-                     nullptr, Y, acc_debug, stream);
+                     nullptr, GemmChoice{}, Y, acc_debug, stream);
 }
 
 hq_status hq_forward_host(const hq_layer_desc* desc, const uint16_t* X_host, int64_t T,
@@ -1728,14 +1810,17 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
   if (s == HQ_OK) s = check_epilogue(epilogue, T, desc->N, Y);
   if (s != HQ_OK || T == 0) return s;
   if (T > kMaxEpRows || desc->N > kMaxEpCols) return HQ_ERR_UNSUPPORTED;
-  // a few tokens: one pass over the weights (the weight-only form's transform
-  // and the raw accumulators need the tiles)
-  if (few_tokens(T, desc->N, desc->K, desc->code_format != HQ_CODES_I8) && desc->out_order <= 1 &&
-      acc_debug == nullptr) {
-    DeviceState* dev;
-    s = device_state(&dev);
-    if (s != HQ_OK) return s;
-    const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
+  DeviceState* dev;
+  s = device_state(&dev);
+  if (s != HQ_OK) return s;
+  const bool plain = plain_epilogue(epilogue);
+  hq_product_plan plan;
+  s = plan_product(shape_of(desc, T, plain, epilogue != nullptr && epilogue->act != HQ_ACT_NONE,
+                            acc_debug != nullptr),
+                   dev->sm_count, pair_clusters(dev), &plan);
+  if (s != HQ_OK) return s;
+  const bool packed = desc->code_format == HQ_CODES_I4_PACKED;
+  if (plan.kernel == HQ_PRODUCT_ROWS) {
     RowsParams p;
     std::memset(&p, 0, sizeof(p));
     p.A = reinterpret_cast<const uint8_t*>(a_codes);
@@ -1752,34 +1837,29 @@ hq_status hq_linear_ep(const hq_layer_desc* desc, int64_t T, const int8_t* a_cod
     p.colsum = colsum;
     p.bias = bias_f32;
     set_rows_epilogue(&p, epilogue, Y);
-    return from_cuda(launch_rows(packed ? 2 : 1, p, dev->sm_count,
+    return from_cuda(launch_rows(packed ? 2 : 1, p, plan.split,
                                  reinterpret_cast<cudaStream_t>(stream)));
   }
-  // too few tiles for the GPU: K split over a cluster (codes one per byte)
-  if (desc->out_order <= 1 && acc_debug == nullptr && desc->code_format == HQ_CODES_I8) {
-    DeviceState* dev;
-    s = device_state(&dev);
-    if (s != HQ_OK) return s;
-    const SplitKPlan pl = splitk_plan(T, desc->N, desc->K, dev->sm_count);
-    double tiles_us;
-    (void)choose_gemm_ep(T, desc->N, desc->K, dev->sm_count, pair_clusters(dev), 0, false,
-                         epilogue != nullptr && epilogue->act != HQ_ACT_NONE, &tiles_us);
-    if (pl.us < tiles_us) {
-      SplitKParams p;
-      std::memset(&p, 0, sizeof(p));
-      p.a_scale = a_scale;
-      p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
-      p.a_mean = a_mean;
-      p.w_scale = w_scale;
-      p.colsum = colsum;
-      p.bias = bias_f32;
-      set_rows_epilogue(&p, epilogue, Y);
-      return run_splitk(dev, pl, false, a_codes, T, w_codes, desc->N, desc->K, &p,
-                        reinterpret_cast<cudaStream_t>(stream));
-    }
+  if (plan.kernel == HQ_PRODUCT_SPLIT) {
+    SplitKParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.a_scale = a_scale;
+    p.a_scale_per_row = desc->act_gran == HQ_PER_TOKEN ? 1 : 0;
+    p.a_mean = a_mean;
+    p.w_scale = w_scale;
+    p.colsum = colsum;
+    p.bias = bias_f32;
+    set_rows_epilogue(&p, epilogue, Y);
+    return run_splitk(dev, plan, false, a_codes, T, w_codes, desc->N, desc->K, &p,
+                      reinterpret_cast<cudaStream_t>(stream));
   }
-  return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32,
-                     plain_epilogue(epilogue) ? nullptr : epilogue, Y, acc_debug, stream);
+  // (forced tiles run a plain epilogue too)
+  const hq_epilogue none{};
+  const hq_epilogue* ep = plan.kernel == HQ_PRODUCT_LINEAR ? nullptr
+                          : epilogue != nullptr            ? epilogue
+                                                           : &none;
+  return linear_impl(desc, T, a_codes, a_scale, a_mean, w_codes, w_scale, colsum, bias_f32, ep,
+                     GemmChoice{plan.kernel == HQ_PRODUCT_PAIR, plan.width}, Y, acc_debug, stream);
 }
 
 hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, const uint16_t* W,
@@ -1804,7 +1884,12 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
   if (s != HQ_OK) return s;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int KB = 2 * K;  // bytes per row of X and W
-  if (few_tokens(T, N, KB, false)) {  // one pass over W
+  hq_product_plan plan;
+  s = plan_product(ProductShape{T, N, KB, true, false, 0,
+                                epilogue != nullptr && epilogue->act != HQ_ACT_NONE, false, false},
+                   dev->sm_count, pair_clusters(dev), &plan);
+  if (s != HQ_OK) return s;
+  if (plan.kernel == HQ_PRODUCT_ROWS) {
     RowsParams p;
     std::memset(&p, 0, sizeof(p));
     p.A = reinterpret_cast<const uint8_t*>(X);
@@ -1815,20 +1900,16 @@ hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, cons
     p.N = N;
     p.bias16 = bias;
     set_rows_epilogue(&p, epilogue, Y);
-    return from_cuda(launch_rows(0, p, dev->sm_count, st));
+    return from_cuda(launch_rows(0, p, plan.split, st));
   }
-  const SplitKPlan pl = splitk_plan(T, N, KB, dev->sm_count);
-  double tiles_us;
-  const GemmChoice gc =
-      choose_gemm_ep(T, N, KB, dev->sm_count, pair_clusters(dev), 0, false,
-                     epilogue != nullptr && epilogue->act != HQ_ACT_NONE, &tiles_us);
-  if (pl.us < tiles_us) {  // too few tiles for the GPU
+  if (plan.kernel == HQ_PRODUCT_SPLIT) {
     SplitKParams p;
     std::memset(&p, 0, sizeof(p));
     p.bias16 = bias;
     set_rows_epilogue(&p, epilogue, Y);
-    return run_splitk(dev, pl, true, X, T, W, N, KB, &p, st);
+    return run_splitk(dev, plan, true, X, T, W, N, KB, &p, st);
   }
+  const GemmChoice gc{plan.kernel == HQ_PRODUCT_PAIR, plan.width};
   const int bn = gc.bn;
   CUtensorMap maps[4];
   if ((s = encode_kmajor_i8(&maps[0], X, T, KB, 128)) != HQ_OK) return s;
@@ -1868,6 +1949,10 @@ hq_status check_gn_desc(const hq_group_norm_desc* d) {
   return HQ_OK;
 }
 
+hq_status check_plan_query(int64_t T, int sms, int pair_clusters, const hq_product_plan* plan) {
+  return T < 1 || sms < 1 || pair_clusters < 0 || plan == nullptr ? HQ_ERR_INVALID_ARGUMENT : HQ_OK;
+}
+
 // The workspace depends on the current device's SM count where there is one.
 int sms_or_default() {
   DeviceState* dev;
@@ -1876,6 +1961,41 @@ int sms_or_default() {
 }  // namespace
 
 extern "C" {
+
+hq_status hq_debug_dense_plan(const hq_dense_desc* desc, int64_t T, int act, int sms,
+                              int pair_clusters, hq_product_plan* plan) {
+  if (desc == nullptr || desc->K <= 0 || desc->N <= 0) return HQ_ERR_INVALID_ARGUMENT;
+  const hq_status s = check_plan_query(T, sms, pair_clusters, plan);
+  if (s != HQ_OK) return s;
+  return plan_product(ProductShape{T, desc->N, 2 * int64_t(desc->K), true, false, 0,
+                                   act != HQ_ACT_NONE, false, false},
+                      sms, pair_clusters, plan);
+}
+
+hq_status hq_debug_linear_ep_plan(const hq_layer_desc* desc, int64_t T, int plain, int act, int sms,
+                                  int pair_clusters, hq_product_plan* plan) {
+  if (desc == nullptr || desc->K <= 0 || desc->N <= 0 || desc->out_order < 0)
+    return HQ_ERR_INVALID_ARGUMENT;
+  const hq_status s = check_plan_query(T, sms, pair_clusters, plan);
+  if (s != HQ_OK) return s;
+  const ProductShape q = shape_of(desc, T, plain != 0, act != HQ_ACT_NONE, false);
+  if (q.logo < 0) return HQ_ERR_UNSUPPORTED;
+  return plan_product(q, sms, pair_clusters, plan);
+}
+
+hq_status hq_debug_set_product_plan(const hq_product_plan* plan) {
+  const hq_product_plan p = plan != nullptr ? *plan : hq_product_plan{};
+  const int w = p.width, k = p.split;
+  bool ok = p.kernel == HQ_PRODUCT_AUTO || p.kernel == HQ_PRODUCT_ROWS;
+  if (p.kernel == HQ_PRODUCT_SPLIT)
+    ok = (w == 16 || w == 32 || w == 64 || w == 128) && (k == 1 || k == 2 || k == 4 || k == 8);
+  if (p.kernel == HQ_PRODUCT_TILES) ok = w == 64 || w == 128 || w == 192 || w == 256;
+  if (p.kernel == HQ_PRODUCT_PAIR) ok = w == 128 || w == 192 || w == 256;
+  if (!ok) return HQ_ERR_INVALID_ARGUMENT;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  g_product_plan = p;
+  return HQ_OK;
+}
 
 size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, int64_t S) {
   if (check_gn_desc(desc) != HQ_OK || B <= 0 || S <= 0) return 0;

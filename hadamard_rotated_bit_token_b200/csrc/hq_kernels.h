@@ -174,8 +174,10 @@ struct RowsParams {
   int64_t gate_rows;
   uint16_t* Y;               // [T,N]
 };
-// kind: 0 bf16, 1 int8 codes, 2 packed codes of A.
-cudaError_t launch_rows(int kind, RowsParams p, int sms, cudaStream_t st);
+// kind: 0 bf16, 1 int8 codes, 2 packed codes of A; wk: rows_warps().
+cudaError_t launch_rows(int kind, RowsParams p, int wk, cudaStream_t st);
+// How many warps share the K of a group of rows: 1, 2 or 4.
+int rows_warps(int T, int N, int64_t row_bytes, int sms);
 
 // The same with K split over a cluster: hq_splitk.cu.
 struct SplitKParams {
@@ -206,8 +208,12 @@ struct SplitKParams {
 // modelled time (1e30: no plan).
 struct SplitKPlan {
   double us;
-  int nt, log_split, tiles, k_blocks;
+  int nt, log_split;
 };
+// Output tiles of nt tokens x 128 columns.
+inline int64_t splitk_tiles(int64_t T, int N, int nt) {
+  return (T + nt - 1) / nt * ((int64_t(N) + 127) / 128);
+}
 // Microseconds in which N rows of weights arrive: from L2 what it keeps, at the
 // memory's rate beyond.
 inline double weights_us(int64_t N, int64_t row_bytes) {

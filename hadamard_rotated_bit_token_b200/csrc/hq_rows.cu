@@ -203,6 +203,10 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsParams p) 
 
 namespace {
 
+// Rows of B a warp: two for one or two tokens; four for more, which halves the
+// tokens' reads from L1.
+constexpr int rows_per_warp(int T) { return T > 2 ? 4 : 2; }
+
 template <int KIND, int TT, int R>
 cudaError_t launch_one(const RowsParams& p, cudaStream_t st) {
   const int rows = R << p.log_wr;
@@ -210,41 +214,39 @@ cudaError_t launch_one(const RowsParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <int KIND, int TT>
-cudaError_t launch_r(const RowsParams& p, int r, cudaStream_t st) {
-  return r == 4 ? launch_one<KIND, TT, 4>(p, st) : launch_one<KIND, TT, 2>(p, st);
-}
-
 template <int KIND>
-cudaError_t launch_tt(const RowsParams& p, int r, cudaStream_t st) {
-  if (p.T == 1) return launch_r<KIND, 1>(p, r, st);
-  if (p.T == 2) return launch_r<KIND, 2>(p, r, st);
-  if (p.T <= 4) return launch_r<KIND, 4>(p, r, st);
-  return launch_r<KIND, 8>(p, r, st);
+cudaError_t launch_tt(const RowsParams& p, cudaStream_t st) {
+  if (p.T == 1) return launch_one<KIND, 1, rows_per_warp(1)>(p, st);
+  if (p.T == 2) return launch_one<KIND, 2, rows_per_warp(2)>(p, st);
+  if (p.T <= 4) return launch_one<KIND, 4, rows_per_warp(4)>(p, st);
+  return launch_one<KIND, 8, rows_per_warp(8)>(p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_rows(int kind, RowsParams p, int sms, cudaStream_t st) {
-  // Two rows a warp for one or two tokens; four for more, which halves the
-  // tokens' reads from L1.  K is shared between two or four warps while there
-  // are fewer than eight warps an SM, and up to sixteen where it leaves each the
-  // four steps it keeps in flight.  (Measured over 1152..16384 outputs and 256..
-  // 4608 inputs; within 10 % of the best of the six choices.)
-  const int r = p.T > 2 ? 4 : 2;
+int rows_warps(int T, int N, int64_t row_bytes, int sms) {
+  // K is shared between two or four warps while there are fewer than eight warps
+  // an SM, and up to sixteen where it leaves each the four steps it keeps in
+  // flight.  (Measured over 1152..16384 outputs and 256..4608 inputs; within 10 %
+  // of the best of the six choices of this and of the rows a warp.)
+  const int r = rows_per_warp(T);
   int log_wk = 0;
-  while (log_wk < 2 && (int64_t(2) << log_wk) * 512 <= p.row_bytes) {
-    const int64_t warps = (int64_t(p.N) / r) << log_wk;
+  while (log_wk < 2 && (int64_t(2) << log_wk) * 512 <= row_bytes) {
+    const int64_t warps = (int64_t(N) / r) << log_wk;
     if (warps >= 16 * int64_t(sms) ||
-        (warps >= 8 * int64_t(sms) && (int64_t(2) << log_wk) * 2048 > p.row_bytes))
+        (warps >= 8 * int64_t(sms) && (int64_t(2) << log_wk) * 2048 > row_bytes))
       break;
     ++log_wk;
   }
-  p.log_wr = 2 - log_wk;
+  return 1 << log_wk;
+}
+
+cudaError_t launch_rows(int kind, RowsParams p, int wk, cudaStream_t st) {
+  p.log_wr = wk == 1 ? 2 : wk == 2 ? 1 : 0;
   switch (kind) {
-    case kRowsBF16: return launch_tt<kRowsBF16>(p, r, st);
-    case kRowsI8: return launch_tt<kRowsI8>(p, r, st);
-    default: return launch_tt<kRowsI4>(p, r, st);
+    case kRowsBF16: return launch_tt<kRowsBF16>(p, st);
+    case kRowsI8: return launch_tt<kRowsI8>(p, st);
+    default: return launch_tt<kRowsI4>(p, st);
   }
 }
 

@@ -410,7 +410,7 @@ SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms) {
   const double arrive = weights_us(N, row_bytes);
   for (int nt : {16, 32, 64, 128}) {
     if (nt > 16 && nt >= 2 * T) break;
-    const int64_t tiles = (T + nt - 1) / nt * ((N + kSkRows - 1) / kSkRows);
+    const int64_t tiles = splitk_tiles(T, N, nt);
     for (int ls = 0; ls <= 3 && (1 << ls) <= k_blocks; ++ls) {
       if ((tiles << ls) > 4 * int64_t(sms)) break;
       double f = double(tiles << ls) / sms;
@@ -422,7 +422,7 @@ SplitKPlan splitk_plan(int64_t T, int N, int64_t row_bytes, int sms) {
       double product = 0.2 * ((k_blocks >> ls) + 1) * f;
       if (product < arrive) product = arrive;
       const double us = 3.9 + product + (0.03 * nt + 0.055 * (nt >> ls)) * f;
-      if (us < best.us) best = SplitKPlan{us, nt, ls, int(tiles), k_blocks};
+      if (us < best.us) best = SplitKPlan{us, nt, ls};
     }
   }
   return best;

@@ -127,6 +127,49 @@ hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64
                         const uint16_t* gamma, const uint16_t* beta, uint16_t* Y, void* workspace,
                         size_t workspace_bytes, hq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Test hooks: which kernel a product with an epilogue runs.
+ *   HQ_PRODUCT_ROWS    one pass over the weights from registers, T <= 8;
+ *                      width: the token count it is built for (1, 2, 4, 8),
+ *                      split: warps that share a row's K (1, 2, 4);
+ *   HQ_PRODUCT_SPLIT   K split over a cluster; width: tokens per tile (16, 32,
+ *                      64, 128), split: CTAs per cluster (1, 2, 4, 8);
+ *   HQ_PRODUCT_TILES   one CTA per 128 x width tile (64, 128, 192, 256);
+ *   HQ_PRODUCT_PAIR    two CTAs per 256 x width tile (128, 192, 256);
+ *   HQ_PRODUCT_LINEAR  hq_linear's own kernel (a plain epilogue on codes);
+ *                      width its tile's, split 2 for the CTA pair.
+ * Where width or split are not named they are 1 in what a query returns, and
+ * not read of what is set. */
+enum {
+  HQ_PRODUCT_AUTO = 0,
+  HQ_PRODUCT_ROWS = 1,
+  HQ_PRODUCT_SPLIT = 2,
+  HQ_PRODUCT_TILES = 3,
+  HQ_PRODUCT_PAIR = 4,
+  HQ_PRODUCT_LINEAR = 5
+};
+typedef struct hq_product_plan {
+  int32_t kernel, width, split;
+} hq_product_plan;
+
+/* Host only (no device call): the plan of hq_dense and hq_linear_ep for T
+ * tokens on a device with `sms` SMs that holds `pair_clusters` CTA-pair
+ * clusters.  act: the epilogue's; plain != 0: there is none (and no raw
+ * accumulators are asked for).  HQ_ERR_UNSUPPORTED where a plan is set that
+ * cannot run the product. */
+hq_status hq_debug_dense_plan(const hq_dense_desc* desc, int64_t T, int act, int sms,
+                              int pair_clusters, hq_product_plan* plan);
+hq_status hq_debug_linear_ep_plan(const hq_layer_desc* desc, int64_t T, int plain, int act, int sms,
+                                  int pair_clusters, hq_product_plan* plan);
+
+/* Host state, applies to calls issued after it: the plan that hq_dense and
+ * hq_linear_ep take instead of choosing one (NULL or HQ_PRODUCT_AUTO: the
+ * default).  They return HQ_ERR_UNSUPPORTED for a product that it cannot run:
+ * ROWS past 8 tokens, SPLIT with fewer 128-byte K blocks than CTAs, PAIR for
+ * packed codes or the weight-only form, ROWS and SPLIT for the weight-only form
+ * or with raw accumulators, SPLIT and 256-column tiles for packed codes. */
+hq_status hq_debug_set_product_plan(const hq_product_plan* plan);
+
 #ifdef __cplusplus
 }
 #endif

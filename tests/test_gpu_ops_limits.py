@@ -102,3 +102,20 @@ def test_tiles_give_up_and_recover(hq, make, T, K, N):
 def test_residual_box_gives_up_and_recovers(hq, make, T, K, N):
     """A box of the residual that never comes."""
     _times_out_and_recovers(hq, *make(hq, T, K, N), hq.HQ_FAULT_TILE_WITHHOLD_RESIDUAL)
+
+
+# every tile kernel (kernel, columns, fault it knows), set by the plan hook
+SET = [(k, w, f) for k, ws in ((3, (64, 128, 192, 256)), (4, (128, 192, 256))) for w in ws
+       for f in ("STAGE", "RESIDUAL") if f == "STAGE" or w <= 192]
+
+
+@pytest.mark.parametrize("make", [_dense, _linear])
+@pytest.mark.parametrize("kernel,width,fault", SET)
+@pytest.mark.parametrize("T,K,N", [(131, 272, 208), (5117, 1168, 1168)])
+def test_every_tile_kernel_gives_up_and_recovers(hq, make, kernel, width, fault, T, K, N):
+    call, want = make(hq, T, K, N)
+    hq.hq_debug_set_product_plan(hq.ProductPlan(kernel, width))
+    try:
+        _times_out_and_recovers(hq, call, want, getattr(hq, f"HQ_FAULT_TILE_WITHHOLD_{fault}"))
+    finally:
+        hq.hq_debug_set_product_plan(None)
