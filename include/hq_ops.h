@@ -34,9 +34,13 @@ extern "C" {
  *   HQ_ACT_SILU       z / (1 + e^-z)
  *   HQ_ACT_GELU       z Phi(z) = z (1 + erf(z / sqrt 2)) / 2
  *   HQ_ACT_GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
- * A NaN stays a NaN.  Silu and the gelus are taken to |error| <= 2^-20 (2^-16
- * for HQ_ACT_GELU) of their value, plus 4e-18 (1.1e-7 for HQ_ACT_GELU); of
- * -infinity they give their limit to that error. */
+ * A NaN stays a NaN.  In fp32, before the stored rounding, silu and gelu_tanh are
+ * z sigmoid(u), with u = z and u = 2 sqrt(2/pi) (z + 0.044715 z^3), and are off by
+ * at most 2^-20 (1 + |u| / 4) of their value plus 7e-18: the exponential's and the
+ * reciprocal's own error, and the rounding of the exponent, which grows with u
+ * (|u| <= 44; the value itself is within 7e-18 of 0 from u = -43.3 down).  HQ_ACT_GELU is off by at most
+ * 2^-16 of its value plus 1.1e-7 (the fit of its exponent).  Of -infinity they give
+ * their limit to that error. */
 enum {
   HQ_ACT_NONE = 0,
   HQ_ACT_RELU = 1,
