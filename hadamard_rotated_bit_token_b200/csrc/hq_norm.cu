@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "hq_act.cuh"
 #include "hq_device.cuh"
@@ -130,7 +131,9 @@ struct Merge {
 __device__ __forceinline__ float2 mean_rstd(float2 stat, float inv_n, float eps) {
   // the rounding of M2's subtraction can leave a tiny negative value
   const float var = stat.y * inv_n;
-  return make_float2(stat.x, rsqrtf((var < 0.0f ? 0.0f : var) + eps));
+  // squares that overflowed: rsqrt(infinity) = 0 would give beta without a trace
+  const float none = __int_as_float(0x7FFFFFFF);
+  return make_float2(stat.x, var < INFINITY ? rsqrtf((var < 0.0f ? 0.0f : var) + eps) : none);
 }
 
 // x / d for x < 2^16, with magic = ceil(2^32 / d) (0 for d = 1)

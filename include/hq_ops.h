@@ -125,7 +125,9 @@ size_t hq_group_norm_workspace_bytes(const hq_group_norm_desc* desc, int64_t B, 
  * Statistics are held in fp32 as means and sums of squared deviations around a
  * value of the group (never a difference of large sums), in an order that
  * depends on the sizes and the device's SM count alone.  A NaN or an infinity
- * makes its image's group NaN and touches no other.  B = 0 or S = 0 is a no-op.
+ * makes its image's group NaN and touches no other, and so do finite values
+ * whose squared deviations add up past fp32's range (3.4e38; deviations below
+ * 1e-22 count as none).  B = 0 or S = 0 is a no-op.
  * B, S < 2^31.  X, Y, gamma and beta 16-byte aligned. */
 hq_status hq_group_norm(const hq_group_norm_desc* desc, const uint16_t* X, int64_t B, int64_t S,
                         const uint16_t* gamma, const uint16_t* beta, uint16_t* Y, void* workspace,
