@@ -18,8 +18,11 @@
 // Part 0 itself adds n_0 (m_0 - mean)^2 to M2, so (m_0 - mean)^2 n <= M2 n / n_0
 // and the subtraction costs at most a factor n / n_0, the number of parts,
 // whatever the data.  A thread's values of one channel merge the same way
-// around the first of them.  Orders depend on sizes alone; equal values give
-// exactly their mean and M2 = 0.
+// around the first of them, and around their mean so far after every 128 (a
+// first value far from thousands of equal ones: their squares' roundings add up
+// one way, and the factor makes 24 % of the variance of them at 4047 values, 3e-5
+// so).  Orders depend on sizes alone; equal values give exactly their mean and
+// M2 = 0.
 //
 // Why two passes of one CTA an SM, where the tensor does not fit the registers:
 // keeping a few groups at a time resident over a cluster (X read once) was tried
@@ -45,6 +48,8 @@ namespace hq {
 namespace {
 
 constexpr int kGnThreads = 512;
+// A thread's sums move to the mean so far after this many values of a channel.
+constexpr int kRecenter = 128;
 // Per-thread parts: value i of thread t at part[i * kPartLd + t], so a warp
 // stores without bank conflicts (and reads nearly so: the odd pitch).
 constexpr int kPartLd = kGnThreads + 1;
@@ -101,6 +106,18 @@ struct ThreadStats {
         s1[i] = a.x, s1[i + 1] = a.y;
         s2[i] = b.x, s2[i + 1] = b.y;
       }
+    }
+  }
+  // The same sums of n values around their mean instead (or next to it: delta is
+  // what the addition to the pivot made of it).
+  __device__ __forceinline__ void recenter(int n) {
+    const float fn = float(n), inv = rcp_approx(fn);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float to = fmaf(s1[i], inv, piv[i]), delta = to - piv[i];
+      s2[i] = fmaf(-delta, fmaf(-fn, delta, 2.0f * s1[i]), s2[i]);
+      s1[i] = fmaf(-fn, delta, s1[i]);
+      piv[i] = to;
     }
   }
   // (mean, M2) of n values a channel -> this thread's column of `part`
@@ -315,6 +332,7 @@ __global__ void __launch_bounds__(kGnThreads, 1) gn_stats_kernel(const GnParams 
           }
 #pragma unroll
           for (int j = 0; j < U; ++j) ts.add(cur[j]);
+          if ((cnt - left) % kRecenter == 0) ts.recenter(cnt - left);
         }
 #pragma unroll
         for (int j = 0; j < U - 1; ++j)
@@ -327,11 +345,18 @@ __global__ void __launch_bounds__(kGnThreads, 1) gn_stats_kernel(const GnParams 
     } else {
       ThreadStats<VEC> ts;
       ts.start(*reinterpret_cast<const V*>(xs + threadIdx.x * VEC));
-      for (int r = 0; r < rows; ++r, xs += p.C)
+      const int q = nv / kGnThreads, rem = nv % kGnThreads;
+      const int each = int(threadIdx.x) < rem ? q + 1 : q;  // vectors of a row
+      int since = 0;
+      for (int r = 0; r < rows; ++r, xs += p.C) {
         for (int cv = threadIdx.x; cv < nv; cv += kGnThreads)
           ts.add(*reinterpret_cast<const V*>(xs + cv * VEC));
-      const int q = nv / kGnThreads, rem = nv % kGnThreads;
-      ts.finish(rows * (int(threadIdx.x) < rem ? q + 1 : q), part);
+        if ((since += each) >= kRecenter) {
+          ts.recenter((r + 1) * each);
+          since = 0;
+        }
+      }
+      ts.finish(rows * each, part);
       __syncthreads();
       // as one row of kGnThreads vectors, each with the values of its thread
       block_group_stats<VEC>(p, part, sums, 1, kGnThreads, kGnThreads * VEC, 1, inv_n, 0, 0.0f,

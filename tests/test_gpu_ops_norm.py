@@ -60,3 +60,25 @@ def test_large_values_whose_squares_fit(hq, B, S, C, G):
     assert torch.equal(norm(X * 2.0 ** 48), want)
     assert torch.equal(norm(X * 2.0 ** -30), want)
     assert hq.hq_check_device_error() == 0
+
+
+# rows: those that a block's threads start with, one or a few rows a thread
+@pytest.mark.parametrize("B,S,C,G,rows,v", [
+    (1, 1 << 27, 8, 1, 512, 139.0), (1, (1 << 24) + 9, 128, 8, 32, 182.0),
+    (1, 300000, 8192, 1, 1, 182.0), (1, (1 << 26) + 1, 7, 7, 73, 139.0),
+    (2, (1 << 23) + 3, 66, 6, 15, 182.0), (1, (1 << 24) + 9, 128, 8, 3200, 182.0)])
+def test_a_first_value_far_from_thousands_of_equal_ones(hq, B, S, C, G, rows, v):
+    """One value in the threads' first rows of the first chunk, zeros behind: the
+    variance is all that value's, and the squares of the others' distance from it
+    must not swamp it.  Tensors of up to 5 GB, whose statistics are known exactly."""
+    X = torch.zeros(B, S, C, dtype=torch.bfloat16, device="cuda")
+    X[:, :rows] = v
+    Y = hq.GroupNorm(C, G)(X)
+    mean = v * rows / S
+    var = v * v * (rows / S) * (1 - rows / S)
+    for got, x in ((Y[:, :rows], v), (Y[:, rows:rows + 5000], 0.0), (Y[:, -5000:], 0.0)):
+        want = (x - mean) / (var + 1e-5) ** 0.5
+        # one rounding to bf16, and 2^-11 for the statistics
+        assert bool(((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * abs(want)).all()), (
+            x, want, float(got.double().min()), float(got.double().max()))
+    assert hq.hq_check_device_error() == 0
