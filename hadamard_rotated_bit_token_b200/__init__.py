@@ -1055,6 +1055,8 @@ class GroupNorm:
     """A group norm with an activation over channels-last activations
     (hq_group_norm): gamma and beta bf16 [C] or None."""
 
+    KEPT_SIZES = 64  # input sizes whose workspace size is remembered
+
     def __init__(self, channels, groups, gamma=None, beta=None, eps=1e-5, act=HQ_ACT_NONE):
         self.desc = GroupNormDesc(channels, groups, act, eps)
         self.gamma, self.beta = gamma, beta
@@ -1077,6 +1079,8 @@ class GroupNorm:
                 with rt.device_guard(key[0]):
                     nb = hq_group_norm_workspace_bytes(self.desc, key[1],
                                                        n // (key[1] * self.desc.C))
+                if len(self._ws_bytes) >= self.KEPT_SIZES:
+                    self._ws_bytes.clear()
                 self._ws_bytes[key] = nb
             if nb:
                 ws = X.new_empty(nb, dtype=rt.u8)

@@ -276,3 +276,31 @@ def test_a_layers_launches_all_go_to_its_own_device(hq, monkeypatch):
     for layer in (lay, gw):
         with pytest.raises(ValueError, match="device"):
             layer.forward(torch.zeros(4, 64, dtype=torch.bfloat16), Y)
+
+
+def test_group_norm_remembers_a_bounded_number_of_sizes(hq, monkeypatch):
+    """A norm called with a new image size every time does not grow."""
+    torch = pytest.importorskip("torch")
+    import contextlib
+    monkeypatch.setattr(hq, "_rt", type("Runtime", (), dict(
+        device_guard=staticmethod(lambda dev: contextlib.nullcontext()), u8=torch.uint8)))
+    asked = []
+    monkeypatch.setattr(hq, "hq_group_norm", lambda *a: asked.append(a[-1]))
+
+    class Input(_OnDevice):
+        def numel(self):
+            n = 1
+            for k in self.shape:
+                n *= k
+            return n
+
+        def new_empty(self, n, dtype=None):
+            return ("workspace", n)
+
+    norm = hq.GroupNorm(64, 8)
+    for S in range(20000, 21000):
+        X = Input(FAKE, (1, S, 64), torch.bfloat16)
+        norm(X, X)
+    assert len(norm._ws_bytes) <= 64 and len(asked) == 1000
+    want = hq.hq_group_norm_workspace_bytes(norm.desc, 1, 20999)
+    assert want > 0 and asked[-1] == ("workspace", want)
