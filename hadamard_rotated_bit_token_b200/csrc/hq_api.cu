@@ -158,6 +158,8 @@ int g_last_cuda_error = 0;
 hq_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return HQ_OK;
   g_last_cuda_error = int(e);
+  // reported here: not once more by the next launch's cudaGetLastError
+  (void)cudaGetLastError();
   return HQ_ERR_CUDA;
 }
 
