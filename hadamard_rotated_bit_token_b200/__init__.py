@@ -566,13 +566,15 @@ def _epilogue_ref(rt, ep, T, N, dev):
     if ep is None:
         return None
     # both addresses anew at every call: the tensors may have been exchanged or
-    # taken away since the last one
-    ep._residual = _tensor(ep.residual, "residual", rt.bf16, (T, N), dev)
-    ep._gate = None
+    # taken away since the last one.  Each is written once, as another thread's
+    # call may be reading the same object.
+    gate = None
     if ep.gate is not None:
         if ep.gate_rows < 1:
             raise ValueError("a gate needs gate_rows >= 1 (rows of Y per row of the gate)")
-        ep._gate = _tensor(ep.gate, "gate", rt.bf16, (-(-T // ep.gate_rows), N), dev)
+        gate = _tensor(ep.gate, "gate", rt.bf16, (-(-T // ep.gate_rows), N), dev)
+    ep._residual = _tensor(ep.residual, "residual", rt.bf16, (T, N), dev)
+    ep._gate = gate
     return ctypes.byref(ep)
 
 

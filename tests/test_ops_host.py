@@ -304,3 +304,21 @@ def test_group_norm_remembers_a_bounded_number_of_sizes(hq, monkeypatch):
     assert len(norm._ws_bytes) <= 64 and len(asked) == 1000
     want = hq.hq_group_norm_workspace_bytes(norm.desc, 1, 20999)
     assert want > 0 and asked[-1] == ("workspace", want)
+
+
+def test_an_epilogue_shared_by_two_threads_never_loses_its_gate(hq):
+    """A call refreshes the addresses of its epilogue; another thread's call may be
+    reading them, so neither is ever seen without the tensor it has."""
+    torch = pytest.importorskip("torch")
+    written = []
+
+    class Watched(hq.Epilogue):
+        def __setattr__(self, name, value):
+            written.append((name, value))
+            super().__setattr__(name, value)
+
+    bf16 = torch.bfloat16
+    ep = Watched(0, _OnDevice(FAKE, (4, 64), bf16), _OnDevice(FAR, (2, 64), bf16), 2)
+    written.clear()
+    hq._epilogue_ref(type("Runtime", (), {"bf16": bf16}), ep, 4, 64, 0)
+    assert sorted(written) == [("_gate", FAR), ("_residual", FAKE)]
