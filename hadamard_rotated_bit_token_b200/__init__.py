@@ -677,27 +677,34 @@ class _ActivationBuffers:
     def _stream_key(self):
         """The current stream of the layer's device."""
         dev = self.w_codes.get_device()
-        return None if dev < 0 else _runtime().stream_of(dev)
+        return None if dev < 0 else (_rt or _runtime()).stream_of(dev)
 
-    def _set_for(self, T, asked):
-        key = (T, self._stream_key())
+    def _set_for(self, T, asked, stream=None):
+        key = (T, self._stream_key() if stream is None else stream)
         with _buffers_lock:
             b, was_asked = self._bufs.pop(key, (None, False))
             if b is None:
                 b = self._new_buffers(T)
+                own = [k for k, (_, kept) in self._bufs.items() if not kept]
+                if not asked and len(own) >= self.KEPT_SETS:
+                    del self._bufs[own[0]]
             self._bufs[key] = (b, asked or was_asked)  # the newest, last
-            own = [k for k, (_, kept) in self._bufs.items() if not kept]
-            if len(own) > self.KEPT_SETS:
-                del self._bufs[own[0]]
         return b
 
     def buffers(self, T: int):
         """The set that calls with T tokens on the current stream use."""
         return self._set_for(T, True)
 
-    def _call_buffers(self, T: int):
-        """The set of one forward call."""
-        return self._new_buffers(T) if _runtime().capturing() else self._set_for(T, False)
+    def _check_device(self, X):
+        if X.get_device() != self.w_codes.get_device():
+            raise ValueError(f"X must live on the layer's device {self.w_codes.device}, "
+                             f"got {X.device}")
+
+    def _begin_call(self, X):
+        """(stream, buffer set) of one forward call on X."""
+        self._check_device(X)
+        stream, T = self._stream_key(), X.shape[0]
+        return stream, self._new_buffers(T) if _rt.capturing() else self._set_for(T, False, stream)
 
 
 _buffers_lock = threading.Lock()
@@ -715,11 +722,6 @@ def _on_layer_device(method):
             return method(self, *args, **kwargs)
     return call
 
-
-def _check_input_device(layer, X):
-    if X.get_device() != layer.w_codes.get_device():
-        raise ValueError(f"X must live on the layer's device {layer.w_codes.device}, "
-                         f"got {X.device}")
 
 
 class HadamardQuantLinear(_ActivationBuffers):
@@ -781,13 +783,16 @@ class HadamardQuantLinear(_ActivationBuffers):
         return None
 
     @_on_layer_device
-    def quantize(self, X, bufs=None):
-        """Quantizes X into `bufs` (None: buffers(T)) and returns them."""
-        _check_input_device(self, X)
-        b = self.buffers(X.shape[0]) if bufs is None else bufs
-        hq_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, b["a_codes"],
-                        b["a_scale"], b["a_mean"], b["workspace"])
+    def quantize(self, X):
+        """Quantizes X into buffers(T) and returns them."""
+        self._check_device(X)
+        b = self.buffers(X.shape[0])
+        self._quantize(X, b, self._stream_key())
         return b
+
+    def _quantize(self, X, b, stream):
+        hq_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, b["a_codes"],
+                        b["a_scale"], b["a_mean"], b["workspace"], stream=stream)
 
     @_on_layer_device
     def forward(self, X, Y=None, acc_debug=None, epilogue=None):
@@ -796,14 +801,15 @@ class HadamardQuantLinear(_ActivationBuffers):
         T = X.shape[0]
         if Y is None:
             Y = torch.empty((T, self.desc.N), dtype=torch.bfloat16, device=X.device)
-        b = self.quantize(X, self._call_buffers(T))
+        stream, b = self._begin_call(X)
+        self._quantize(X, b, stream)
         mean = b["a_mean"] if self.desc.centering != HQ_CENTER_NONE else None
         if epilogue is not None:
             hq_linear_ep(self.desc, b["a_codes"], b["a_scale"], mean, self.w_codes, self.w_scale,
-                         self.colsum, self.bias_f32, epilogue, Y, acc_debug)
+                         self.colsum, self.bias_f32, epilogue, Y, acc_debug, stream=stream)
             return Y
         hq_linear(self.desc, b["a_codes"], b["a_scale"], mean, self.w_codes, self.w_scale,
-                  self.colsum, self.bias_f32, Y, acc_debug)
+                  self.colsum, self.bias_f32, Y, acc_debug, stream=stream)
         return Y
 
     __call__ = forward
@@ -990,22 +996,26 @@ class GroupWiseQuantLinear(_ActivationBuffers):
                 "workspace": torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None}
 
     @_on_layer_device
-    def quantize(self, X, bufs=None):
-        """Quantizes X into `bufs` (None: buffers(T)) and returns them."""
-        _check_input_device(self, X)
-        b = self.buffers(X.shape[0]) if bufs is None else bufs
-        hq_gw_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, self.l1s,
-                           b["a_codes"], b["a_scale"], b["u"], b["workspace"])
+    def quantize(self, X):
+        """Quantizes X into buffers(T) and returns them."""
+        self._check_device(X)
+        b = self.buffers(X.shape[0])
+        self._quantize(X, b, self._stream_key())
         return b
+
+    def _quantize(self, X, b, stream):
+        hq_gw_quantize_act(self.desc, X, self.sigma_inv if self.use_sigma else None, self.l1s,
+                           b["a_codes"], b["a_scale"], b["u"], b["workspace"], stream=stream)
 
     @_on_layer_device
     def forward(self, X, Y=None):
         import torch
         if Y is None:
             Y = torch.empty((X.shape[0], self.desc.N), dtype=torch.bfloat16, device=X.device)
-        b = self.quantize(X, self._call_buffers(X.shape[0]))
+        stream, b = self._begin_call(X)
+        self._quantize(X, b, stream)
         hq_gw_linear(self.desc, b["a_codes"], b["a_scale"], b["u"], self.w_codes, self.w_scale,
-                     self.l2b, self.bias_f32, Y, T=X.shape[0])
+                     self.l2b, self.bias_f32, Y, T=X.shape[0], stream=stream)
         return Y
 
     __call__ = forward

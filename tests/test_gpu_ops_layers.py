@@ -110,3 +110,16 @@ def test_buffers_hold_what_the_last_call_on_this_stream_left(hq):
     assert torch.equal(layer.buffers(T)["a_codes"], codes)
     layer(X2)
     assert not torch.equal(layer.buffers(T)["a_codes"], codes)
+
+
+@pytest.mark.parametrize("shape", [(0, 5, 256), (2, 0, 256), (0, 256), (1, 256), (1, 1, 1, 256)])
+def test_block_of_no_or_one_pixel(hq, shape):
+    g = _gen(4)
+    C = 256
+    layer = hq.HadamardQuantLinear(hq.LayerDesc(C, C, 128, a_bits=8, w_bits=8), _bf(g, C, C))
+    X = _bf(g, *shape)
+    Y = hq.PointwiseBlock(hq.GroupNorm(C, 32), layer, residual=True)(X)
+    assert Y.shape == X.shape and bool(Y.isfinite().all())
+    Y = hq.PointwiseBlock(hq.GroupNorm(C, 32), layer, act=hq.HQ_ACT_RELU)(X)
+    assert Y.shape == X.shape and bool((Y >= 0).all())
+    assert hq.hq_check_device_error() == 0
