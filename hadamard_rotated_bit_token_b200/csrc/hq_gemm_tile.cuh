@@ -490,8 +490,8 @@ __device__ __forceinline__ void epi_tile(const GemmParams& p, const CUtensorMap*
 //     32 x 32 box each, so that the operands keep four stages of 48 KB (six of
 //     32 KB in the pair); R comes from global memory into registers one chunk
 //     ahead.  For long main loops: 16384 x 4096 x 8192 in bf16 takes 742-800 us
-//     so (the clock under load varies), 843-869 us with sixteen warps, 64 KB of
-//     boxes and four stages.  In between, 16384 x 1152 x 4608 in bf16: 134 us by
+//     so in short runs (870 where the power cap holds the clock down), 843-869 us
+//     with sixteen warps, 64 KB of boxes and four stages.  In between, 16384 x 1152 x 4608 in bf16: 134 us by
 //     the lean pair, 148 by the wide pair of 192 columns.
 // (Stores from registers, 32 bytes a thread and row, were tried: the 32
 // single-sector accesses of a warp instruction made the epilogue of a 128 x 256

@@ -30,10 +30,13 @@
 // unit of work paid a load, a cluster barrier and a store one after the other.
 // Streaming takes 26.0 us (42 MB read, read again mostly from L2, 42 MB written:
 // 3.2 TB/s of X read once and Y written) and 38.0 us (67 MB in, 67 MB out: 3.5
-// TB/s).  The statistics pass runs near the memory's rate; the normalization is
-// bound by issue slots and special functions (about 120 instructions for 8
-// channels with silu), and two CTAs an SM, or one, two or three rows a batch,
-// made it slower (28 to 30 us).
+// TB/s).  Neither pass is at a limit of the hardware: the statistics read 42 MB in
+// 12.7 us (3.3 TB/s, half of what a copy reaches) with 39 % of the issue slots used,
+// the normalization (about 120 instructions for 8 channels with silu) has issue
+// slots and special functions half busy.  Both wait for their own 16 warps an SM,
+// whose loads in flight and dependent instructions do not cover the latencies.
+// Two CTAs an SM, or one, two or three rows a batch, made the second slower (28 to
+// 30 us).
 #include <cuda_bf16.h>
 
 #include <atomic>

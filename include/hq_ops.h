@@ -96,7 +96,8 @@ typedef struct hq_dense_desc {
  * Output:  Y bf16 [T,N]; it overlaps no input but the residual it may equal.
  * T >= 0 (T = 0 is a no-op), T <= 2^31 - 256.  All pointers 16-byte aligned.
  * Results are deterministic: every sum over K is taken in an order that
- * depends on the sizes and the device's SM count alone. */
+ * depends on the sizes, on whether there is an activation (the kernel's choice
+ * goes by it) and on the device's SM count alone. */
 hq_status hq_dense(const hq_dense_desc* desc, const uint16_t* X, int64_t T, const uint16_t* W,
                    const uint16_t* bias, const hq_epilogue* epilogue, uint16_t* Y,
                    hq_stream_t stream);
