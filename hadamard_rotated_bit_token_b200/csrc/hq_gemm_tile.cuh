@@ -511,9 +511,7 @@ struct ResStream {
 
 // Lane 0: asks for R's box at (row0, col0), if it lies inside R.
 __device__ __forceinline__ void res_load(const GemmEpParams& p, ResStream& s, int row0, int col0) {
-  if (p.withhold == kWithholdResidual && s.issued == 0) {
-    // (the test hook's box that never comes)
-  } else if (row0 < p.T && col0 < p.N) {
+  if (row0 < p.T && col0 < p.N) {
     mbar_arrive_expect_tx(s.bar, kEpBox);
     tma_load_2d(s.box, s.tmR, col0, row0, s.bar);
   } else {
@@ -756,13 +754,15 @@ __device__ __forceinline__ const uint16_t* gate_row_of(const GemmEpParams& p, in
 
 namespace {
 
-// Whether the test hook keeps the producer from loading stage `issued`.
+// Arrivals beyond the usual one that a barrier of this kind waits for: one that
+// never comes where the test hook asks for it, else none.  (A branch in the
+// producer's loop instead cost the pair 3 us of 38.)
 template <bool EP>
-__device__ __forceinline__ bool withheld(const GemmArgs<EP>& p, int issued) {
+__device__ __forceinline__ uint32_t withheld(const GemmArgs<EP>& p, int what) {
   if constexpr (EP)
-    return p.withhold == kWithholdStage && issued == 0;
+    return p.withhold == what ? 1u : 0u;
   else
-    return false;
+    return 0u;
 }
 
 // The copies into the last two parameter slots, of `n` in all, have landed.
@@ -849,7 +849,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
   fence_proxy_async_smem();  // the zeros precede the ring's bulk copies
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + (s == 0 ? withheld<EP>(p, kWithholdStage) : 0u));
       mbar_init(&empty[s], 1);
       if (PK) mbar_init(&conv[s], kConvWarps);  // one arrival per converter warp
     }
@@ -861,7 +861,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
     }
     mbar_init(drain, 1);
     if constexpr (C::WIDE)
-      for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
+      for (int i = 0; i < C::EPW; ++i)
+        mbar_init(&rbar[i], 1 + withheld<EP>(p, kWithholdResidual));
     *abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tmap(tmA);
@@ -907,15 +908,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap* tmA, const CUtensor
             ok = false;
             break;
           }
-          if (!withheld<EP>(p, issued)) {
-            mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
-            if constexpr (PK)  // K bytes of packed A per stage: BK / 2 (a multiple of 16)
-              tma_load_2d(sP + size_t(stage) * C::P_BYTES, tmA, kb * (BK / 2), m_idx * BM,
-                          &full[stage]);
-            else
-              tma_load_2d(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, m_idx * BM, &full[stage]);
-            tma_load_2d(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, n_idx * BN, &full[stage]);
-          }
+          mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
+          if constexpr (PK)  // K bytes of packed A per stage: BK / 2 (a multiple of 16)
+            tma_load_2d(sP + size_t(stage) * C::P_BYTES, tmA, kb * (BK / 2), m_idx * BM,
+                        &full[stage]);
+          else
+            tma_load_2d(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, m_idx * BM, &full[stage]);
+          tma_load_2d(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, n_idx * BN, &full[stage]);
           ++issued;
           if (++stage == C::STAGES) {
             stage = 0;
@@ -1222,7 +1221,7 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
   fence_proxy_async_smem();  // the zeros precede the ring's bulk copies
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + (s == 0 ? withheld<EP>(p, kWithholdStage) : 0u));
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -1233,7 +1232,8 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
     }
     mbar_init(drain, 1);
     if constexpr (C::WIDE)
-      for (int i = 0; i < C::EPW; ++i) mbar_init(&rbar[i], 1);
+      for (int i = 0; i < C::EPW; ++i)
+        mbar_init(&rbar[i], 1 + withheld<EP>(p, kWithholdResidual));
     *abort_flag = 0;
     issued_by[0] = issued_by[1] = 0;
     fence_mbarrier_init();
@@ -1286,12 +1286,10 @@ __device__ __forceinline__ void gemm_pair_body(const CUtensorMap* tmA, const CUt
             ok = false;
             break;
           }
-          if (!withheld<EP>(p, issued)) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
-            const uint32_t bar = full0 + uint32_t(stage) * 8u;
-            tma_load_2d_pair(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, a_row, bar);
-            tma_load_2d_pair(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, b_row, bar);
-          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+          const uint32_t bar = full0 + uint32_t(stage) * 8u;
+          tma_load_2d_pair(sA + size_t(stage) * C::A_BYTES, tmA, kb * BK, a_row, bar);
+          tma_load_2d_pair(sB + size_t(stage) * C::B_BYTES, tmB, kb * BK, b_row, bar);
           ++issued;
           if (++stage == C::STAGES) {
             stage = 0;

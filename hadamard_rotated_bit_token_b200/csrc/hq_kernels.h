@@ -131,9 +131,9 @@ struct GemmEpParams : GemmParams {
   const uint16_t* gate;      // bf16 [ceil(T / gate_rows), N] or null
   int64_t gate_rows;         // rows of Y per row of the gate
   const uint16_t* bias16;    // bf16 operands: bf16 bias [N] or null (p.bias is null)
-  int withhold;              // test hook: 0, or a copy that each CTA leaves out
+  int withhold;              // test hook: 0, or a wait that never ends by itself
 };
-constexpr int kWithholdStage = 1, kWithholdResidual = 2;  // its first stage; its first boxes of R
+constexpr int kWithholdStage = 1, kWithholdResidual = 2;  // for stage 0; for the boxes of R
 
 // As launch_gemm / launch_gemm_pair.  maps: four CUtensorMap, A and B as there,
 // then Y and the residual (without one: any map) [T,N] bf16 with box {64, 32}
@@ -185,7 +185,7 @@ struct SplitKParams {
   int N;
   int log_split, k_blocks, num_n_tiles;
   int stages, log_nt;        // (launch_splitk)
-  int withhold;              // test hook: 1 leaves each CTA's first stage unloaded
+  int withhold;              // test hook: 1: the wait for stage 0 never ends by itself
   // integer codes
   const float* a_scale;      // [T] or [1]
   int a_scale_per_row;

@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kSkThreads, 2)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (warp == 0) {
     if (lane == 0) {
-      for (int s = 0; s < 2 * stages + 1; ++s) mbar_init(&full[s], 1);  // full, empty, tfull
+      for (int s = 0; s < 2 * stages + 1; ++s)  // full, empty, tfull
+        mbar_init(&full[s], s == 0 && p.withhold ? 2 : 1);
       *failed = 0;
       fence_mbarrier_init();
     }
@@ -206,12 +207,10 @@ __global__ void __launch_bounds__(kSkThreads, 2)
           *failed = 1;
           break;
         }
-        if (!p.withhold || i > 0) {  // (withhold: the test hook's stage that never comes)
-          const int x = (kb0 + i) * 128;
-          mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
-          tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, x, n0, &full[stage]);
-          tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, x, t0, &full[stage]);
-        }
+        const int x = (kb0 + i) * 128;
+        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+        tma_load_2d(sW + size_t(stage) * C::W_BYTES, &tmW, x, n0, &full[stage]);
+        tma_load_2d(sX + size_t(stage) * C::X_BYTES, &tmX, x, t0, &full[stage]);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;

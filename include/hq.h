@@ -304,15 +304,15 @@ hq_status hq_debug_set_gemm_variant(int variant);
  *       the first tile are never released.  The kernel records
  *       HQ_ERR_TIMEOUT, waits for the copies it did issue and exits.
  *   HQ_FAULT_SPLITK_WITHHOLD_STAGE (2)   in each CTA of the next products with
- *       an epilogue that split K over a cluster (hq_ops.h), the copy of the
- *       first operand stage is never issued, so the tensor cores' bounded wait
- *       for it expires.  The kernel records HQ_ERR_TIMEOUT, waits for the
- *       copies it did issue and exits;
+ *       an epilogue that split K over a cluster (hq_ops.h), the barrier of the
+ *       first operand stage is set up for one arrival too many, so the tensor
+ *       cores' bounded wait for the stage expires although its copies land.  The
+ *       kernel records HQ_ERR_TIMEOUT, waits for the copies in flight and exits;
  *   HQ_FAULT_TILE_WITHHOLD_STAGE (3)     the same in the products with an
  *       epilogue that take whole output tiles;
- *   HQ_FAULT_TILE_WITHHOLD_RESIDUAL (4)  there the copy of each epilogue warp's
- *       first box of the residual (with tiles of up to 192 columns; wider ones
- *       read the residual without a wait).
+ *   HQ_FAULT_TILE_WITHHOLD_RESIDUAL (4)  there the barriers of the epilogue
+ *       warps' boxes of the residual (with tiles of up to 192 columns; wider
+ *       ones read the residual without a wait).
  * Host state, applies to launches issued after the call. */
 enum {
   HQ_FAULT_NONE = 0,

@@ -1,6 +1,6 @@
-"""GPU tests of the products' bounded waits: a wait that runs out (the copy it
-waits for is withheld by a test hook; nothing faults) is reported, the kernel
-ends by itself, and the next call is right.  Needs a B200."""
+"""GPU tests of the products' bounded waits: a wait that runs out (a test hook
+withholds an arrival; nothing faults) is reported, the kernel ends by itself, and
+the next call is right.  Needs a B200."""
 import contextlib
 
 import pytest
