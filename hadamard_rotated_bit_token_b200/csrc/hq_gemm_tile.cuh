@@ -491,8 +491,8 @@ __device__ __forceinline__ void epi_tile(const GemmParams& p, const CUtensorMap*
 //     32 KB in the pair); R comes from global memory into registers one chunk
 //     ahead.  For long main loops: 16384 x 4096 x 8192 in bf16 takes 742-800 us
 //     so in short runs (870 where the power cap holds the clock down), 843-869 us
-//     with sixteen warps, 64 KB of boxes and four stages.  In between, 16384 x 1152 x 4608 in bf16: 134 us by
-//     the lean pair, 148 by the wide pair of 192 columns.
+//     with sixteen warps, 64 KB of boxes and four stages.  In between, 16384 x 1152
+//     x 4608 in bf16: 134 us by the lean pair, 148 by the wide pair of 192 columns.
 // (Stores from registers, 32 bytes a thread and row, were tried: the 32
 // single-sector accesses of a warp instruction made the epilogue of a 128 x 256
 // tile 11000 cycles instead of 7000.  Sixteen warps of 32 columns on tiles of
